@@ -388,6 +388,172 @@ mla_status_t mla_indexer_topk(const uint16_t* q_idx, const float* head_w, const 
                               int block_size, int topk, int32_t* topk_out, float* scores_out, int max_context_len,
                               void* workspace, size_t workspace_bytes, mla_stream_t stream);
 
+/*
+ * Block tables and slot maps from request lengths, built on the device.
+ * Request b holds context_lens[b] tokens in its first ceil(context_lens[b] /
+ * block_size) blocks and gets new_lens[b] more (0 for one that waits; a
+ * negative length counts as 0).  The blocks that it then lacks are taken from
+ * a ring of free block ids, request by request and in order, and written
+ * behind its last one in its row of the block table; every new token's
+ * position and slot follow:
+ *
+ *   query_start[b] = sum of new_lens before b, query_start[batch] = their sum
+ *   positions[query_start[b] + j]    = context_lens[b] + j
+ *   slot_mapping[query_start[b] + j] = block * block_size + position % block_size
+ *
+ * as the quantize-on-write entry points read them.  Entries behind the last
+ * token are -1 in both, so a call captured at a fixed num_slots serves any
+ * smaller number of tokens.  Tokens past num_slots are left out: they count
+ * in no output.
+ *
+ * The ring's entries free_state[0] (head) to free_state[1] (tail) - 1, each
+ * taken modulo free_capacity, are the free blocks; a call takes from the head
+ * and the caller returns blocks at the tail.  When it runs short, what is
+ * left goes to the first requests: a block that could not be had is -1 in
+ * the table, its tokens' slots are -1, and context_lens_out counts a
+ * request's tokens up to the first such block only.  The same holds for
+ * tokens past max_blocks_per_req blocks.  An entry of the table or the ring
+ * outside [0, num_blocks) gives its tokens slot -1.
+ *
+ *   context_lens      device int32 [batch], new_lens device int32 [batch]
+ *   block_table       device int32 [batch, max_blocks_per_req], in and out:
+ *                     only entries of new blocks are written
+ *   free_blocks       device int32 [free_capacity]
+ *   free_state        device int64 [3]: head, tail (the third is not read)
+ *   slot_mapping      device int64 [num_slots], positions int32 [num_slots]
+ *   query_start       device int32 [batch + 1]
+ *   context_lens_out  device int32 [batch]; may be context_lens
+ *   free_state_out    device int64 [3]: head past the blocks taken, tail,
+ *                     blocks that could not be had; may be free_state
+ * No other two arguments may overlap.
+ */
+mla_status_t mla_block_table_extend(const int32_t* context_lens, const int32_t* new_lens, int batch,
+                                    int32_t* block_table, int max_blocks_per_req, const int32_t* free_blocks,
+                                    int64_t free_capacity, const int64_t* free_state, int64_t num_blocks,
+                                    int block_size, int64_t* slot_mapping, int32_t* positions, int64_t num_slots,
+                                    int32_t* query_start, int32_t* context_lens_out, int64_t* free_state_out,
+                                    mla_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass.  For every token and head, x its head_dim values:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (y = x without a weight)
+ *   the 64 values of y from rope_offset on are rotated in pairs by the angle
+ *   positions[token] * inv_freq[i], i = 0..31:
+ *   (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin)
+ *
+ * where pair i is values 2i and 2i + 1 (interleaved nonzero) or i and i + 32.
+ * Float32 arithmetic, one rounding to bf16 at the end; the angle is kept as a
+ * 64-bit fraction of a turn, exact for any 32-bit position.
+ *
+ *   q, k          head sets on the host, either may be NULL (or have 0 heads)
+ *     in, out     device bf16, 16-byte aligned; head h of token t starts at
+ *                 t * token stride + h * head stride (elements, multiples of
+ *                 8); out may be in with the same strides, else no element
+ *                 of one may be in the other
+ *     weight      device bf16 [head_dim], 16-byte aligned, or NULL: no norm
+ *   head_dim      64..256, a multiple of 8 (wider: MLA_ERR_UNSUPPORTED)
+ *   rope_offset   0..head_dim - 64, a multiple of 8
+ *   eps           > 0
+ *   positions     device int32 [n_tokens]
+ *   inv_freq      device double [32], radians per position
+ * n_tokens == 0 is a no-op.
+ */
+typedef struct {
+  const uint16_t* in;
+  uint16_t* out;
+  int heads;
+  int64_t in_token_stride, in_head_stride, out_token_stride, out_head_stride;
+  const uint16_t* weight;
+} mla_heads_t;
+mla_status_t mla_qk_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t n_tokens, int head_dim,
+                              int rope_offset, int interleaved, float eps, const int32_t* positions,
+                              const double* inv_freq, mla_stream_t stream);
+
+/*
+ * The same pass for a step of the cache: each token's latent is normed, its
+ * 64 key values are rotated, and the row is quantised into the paged cache,
+ * without a bf16 copy of it in memory; the queries' norms and rotation (q, as
+ * above, or NULL) run in the same launch.  The normed latent and the rotated
+ * key are rounded to bf16 before they are quantised, so the cache holds the
+ * bytes that mla_kv_quantize_append writes for those bf16 rows.
+ *
+ *   kv            device bf16 [n_tokens, 512 latent + 64 key], 16-byte
+ *                 aligned, rows kv_token_stride elements apart (a multiple
+ *                 of 8)
+ *   latent_weight device bf16 [512], 16-byte aligned
+ *   slot_mapping, kv_pool, num_blocks, block_size, kv_block_stride, fmt
+ *                 as for mla_kv_quantize_append
+ *   head_dim, rope_offset   of q (ignored without q)
+ * n_tokens == 0 is a no-op.  Two tokens with the same slot race.
+ */
+mla_status_t mla_kv_norm_rope_append(const uint16_t* kv, int64_t kv_token_stride, const uint16_t* latent_weight,
+                                     const mla_heads_t* q, int head_dim, int rope_offset, int interleaved, float eps,
+                                     const int32_t* positions, const double* inv_freq, const int64_t* slot_mapping,
+                                     int64_t n_tokens, void* kv_pool, int64_t num_blocks, int block_size,
+                                     int64_t kv_block_stride, mla_kv_format_t fmt, mla_stream_t stream);
+
+/*
+ * Dense decode over a sliding window and the first tokens.  The q_len query
+ * tokens of request b are the last q_len positions of its context_lens[b]
+ * tokens: token i stands at p = context_lens[b] - q_len + i and sees
+ *
+ *   { t : 0 <= t <= p  and  (t < sinks  or  t > p - window) }
+ *
+ * and out, lse are those of mla_sparse_decode over that set (the same
+ * arithmetic; rows whose logical block is past the table or whose physical
+ * block is outside the pool are not seen; a token that sees nothing gives 0
+ * and -inf).  A window of at least the context is a decode over all of it.
+ * Every row that a token of the call sees is read once per 64 (query token,
+ * head) pairs of its request.
+ *
+ *   q_nope        device bf16 [batch, q_len, num_heads, 512]
+ *   q_rope        device bf16 [batch, q_len, num_heads, 64], 16-byte aligned
+ *   q_len         1..64
+ *   sinks >= 0, window >= 1
+ *   out           device bf16 [batch, q_len, num_heads, 512]
+ *   lse           device float [batch, q_len, num_heads], or NULL
+ *   workspace     at least mla_window_decode_workspace_size(...) bytes,
+ *                 256-byte aligned (that size depends on the current device
+ *                 and may be 0); contents on entry do not matter
+ * All other arguments as for mla_sparse_decode.  batch == 0 is a no-op.
+ */
+size_t mla_window_decode_workspace_size(int batch, int q_len, int num_heads, int max_blocks_per_req, int sinks,
+                                        int window);
+mla_status_t mla_window_decode(const uint16_t* q_nope, const uint16_t* q_rope, const void* kv_pool,
+                               int64_t kv_block_stride, int64_t num_blocks, const int32_t* block_table,
+                               int max_blocks_per_req, const int32_t* context_lens, int batch, int q_len,
+                               int num_heads, int block_size, int sinks, int window, float softmax_scale,
+                               mla_kv_format_t fmt, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * Dense decode of requests that share a prefix.  Every query token of the
+ * batch sees the prefix_len rows of prefix_table and, behind them, its own
+ * request's rows: token i of request b sees own rows t < context_lens[b] -
+ * (q_len - 1 - i), where context_lens[b] counts the tokens after the prefix
+ * (0: the prefix alone).  The prefix is walked once per 64 (request, query
+ * token, head) triples of the whole batch, not once per request, and the two
+ * parts are joined by their LSEs.
+ *
+ *   prefix_table  device int32 [ceil(prefix_len / block_size)] (not read when
+ *                 prefix_len is 0)
+ *   block_table   device int32 [batch, max_blocks_per_req], own blocks
+ *   max_context_len  >= every context_lens[b]; longer ones are cut to it
+ *   workspace     at least mla_prefix_decode_workspace_size(...) bytes,
+ *                 256-byte aligned
+ * All other arguments as for mla_window_decode.
+ */
+size_t mla_prefix_decode_workspace_size(int batch, int q_len, int num_heads, int prefix_len, int max_blocks_per_req,
+                                        int max_context_len);
+mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, const void* kv_pool,
+                               int64_t kv_block_stride, int64_t num_blocks, const int32_t* prefix_table,
+                               int prefix_len, const int32_t* block_table, int max_blocks_per_req,
+                               const int32_t* context_lens, int batch, int q_len, int num_heads, int block_size,
+                               int max_context_len, float softmax_scale, mla_kv_format_t fmt, uint16_t* out,
+                               float* lse, void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,8 @@ __all__ = [
     "mla_indexer_topk_workspace_size", "mla_indexer_topk", "mla_index_key_quantize_append",
     "mla_staged_pool_bytes", "mla_stage_rows_fp8", "mla_sparse_decode_staged_workspace_size",
     "mla_sparse_decode_staged", "mla_sparse_decode_mtp_workspace_size", "mla_sparse_decode_mtp",
+    "mla_block_table_extend", "mla_qk_norm_rope", "mla_kv_norm_rope_append", "mla_window_decode_workspace_size",
+    "mla_window_decode", "mla_prefix_decode_workspace_size", "mla_prefix_decode",
 ]
 
 MLA_KV_NVFP4 = 0
@@ -33,6 +35,14 @@ _lib = None
 
 _STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE_TOO_SMALL",
            4: "MLA_ERR_CUDA"}
+
+
+class _Heads(C.Structure):
+    """mla_heads_t"""
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("heads", C.c_int), ("in_token_stride", C.c_int64),
+                ("in_head_stride", C.c_int64), ("out_token_stride", C.c_int64), ("out_head_stride", C.c_int64),
+                ("weight", C.c_void_p)]
+
 
 # Every symbol include/mla_nvfp4.h declares, with (restype, argtypes).
 _P, _I32, _I64, _SZ, _F32 = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
@@ -65,6 +75,16 @@ SIGNATURES = {
     "mla_sparse_decode_staged_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "mla_sparse_decode_staged": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _F32, _P,
                                         _P, _P, _SZ, _P]),
+    "mla_block_table_extend": (_I32, [_P, _P, _I32, _P, _I32, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _P, _P, _P, _P]),
+    "mla_qk_norm_rope": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _F32, _P, _P, _P]),
+    "mla_kv_norm_rope_append": (_I32, [_P, _I64, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P, _I64, _P, _I64, _I32,
+                                       _I64, _I32, _P]),
+    "mla_window_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "mla_window_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32,
+                                 _P, _P, _P, _SZ, _P]),
+    "mla_prefix_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "mla_prefix_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F32,
+                                 _I32, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -384,3 +404,235 @@ def mla_indexer_topk(q_idx, head_w, idx_key_pool, idx_block_stride, num_blocks, 
                                    topk, _ptr(topk_out), _ptr(scores_out), max_context_len, _ptr(workspace),
                                    ws_bytes, _stream(stream)))
     return topk_out, scores_out
+
+
+# --------------------------------------------------------------------- block tables, norms, dense decodes
+def _here(*tensors) -> torch.device:
+    """The one device of `tensors` (None left out), which has to be the current one."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        device = device or t.device
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    if device is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but cuda:{torch.cuda.current_device()} is the current device")
+    return device
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory whose reuse is ordered behind the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _take(t, shape, dtype, name, device, stream) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _contig(t, dtype, name)
+
+
+def _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt) -> None:
+    if num_blocks > 0 and kv_pool.numel() * kv_pool.element_size() < (num_blocks - 1) * kv_block_stride + \
+            block_size * (352 if fmt == MLA_KV_NVFP4 else 576):
+        raise ValueError("kv_pool does not reach the last row of block num_blocks - 1")
+
+
+def mla_block_table_extend(context_lens, new_lens, block_table, free_blocks, free_state, num_blocks, num_slots,
+                           block_size=64, slot_mapping=None, positions=None, query_start=None, context_lens_out=None,
+                           free_state_out=None, stream=None):
+    """Blocks, positions and slots of every request's new tokens.  context_lens,
+    new_lens int32 [B]; block_table int32 [B, W], extended in place; free_blocks
+    int32 ring with free_state int64 [3] (head, tail, -).  Returns (slot_mapping
+    int64 [num_slots], positions int32 [num_slots], query_start int32 [B + 1],
+    context_lens_out int32 [B], free_state_out int64 [3])."""
+    context_lens = _contig(context_lens, torch.int32, "context_lens")
+    new_lens = _contig(new_lens, torch.int32, "new_lens")
+    block_table = _contig(block_table, torch.int32, "block_table")
+    free_blocks = _contig(free_blocks, torch.int32, "free_blocks")
+    free_state = _contig(free_state, torch.int64, "free_state")
+    dev = _here(context_lens, new_lens, block_table, free_blocks, free_state, slot_mapping, positions, query_start,
+                context_lens_out, free_state_out)
+    batch = context_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != batch or new_lens.numel() != batch or \
+            free_state.numel() != 3:
+        raise ValueError("new_lens [B], block_table [B, W] and free_state [3] must fit context_lens [B]")
+    slot_mapping = _take(slot_mapping, (num_slots,), torch.int64, "slot_mapping", dev, stream)
+    positions = _take(positions, (num_slots,), torch.int32, "positions", dev, stream)
+    query_start = _take(query_start, (batch + 1,), torch.int32, "query_start", dev, stream)
+    context_lens_out = _take(context_lens_out, (batch,), torch.int32, "context_lens_out", dev, stream)
+    free_state_out = _take(free_state_out, (3,), torch.int64, "free_state_out", dev, stream)
+    _check("mla_block_table_extend",
+           load().mla_block_table_extend(_ptr(context_lens), _ptr(new_lens), batch, _ptr(block_table),
+                                         block_table.shape[1], _ptr(free_blocks), free_blocks.numel(),
+                                         _ptr(free_state), num_blocks, block_size, _ptr(slot_mapping),
+                                         _ptr(positions), num_slots, _ptr(query_start), _ptr(context_lens_out),
+                                         _ptr(free_state_out), _stream(stream)))
+    return slot_mapping, positions, query_start, context_lens_out, free_state_out
+
+
+def _heads(x, weight, out, name, stream):
+    """(mla_heads_t, output) of bf16 heads [n, H, D] whose last axis is contiguous."""
+    for t, what in ((x, name), (out, name + "_out")):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{what}: expected torch.bfloat16, got {t.dtype}")
+        if t.dim() != 3 or t.shape != x.shape or (t.numel() > 0 and t.stride(2) != 1):
+            raise ValueError(f"{what} must be [n, heads, dim] with a contiguous last axis, out shaped like in")
+    if weight is not None and _contig(weight, torch.bfloat16, name + "_weight").numel() != x.shape[2]:
+        raise ValueError(f"{name}_weight must have one value for each of {x.shape[2]} dims")
+    if out is None:
+        out = _new(x.shape, torch.bfloat16, x.device, stream)
+    return _Heads(x.data_ptr(), out.data_ptr(), x.shape[1], x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                  None if weight is None else weight.data_ptr()), out
+
+
+def _angles(positions, inv_freq, n):
+    if _contig(positions, torch.int32, "positions").numel() != n:
+        raise ValueError(f"positions must have one entry for each of {n} tokens")
+    if _contig(inv_freq, torch.float64, "inv_freq").numel() != 32:
+        raise ValueError("inv_freq must have 32 entries")
+
+
+def mla_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, rope_offset=0,
+                     interleaved=True, q_out=None, k_out=None, stream=None):
+    """Norm per head (with a weight) and rotation of 64 values from rope_offset
+    on.  q bf16 [n, Hq, D], k bf16 [n, Hk, D] or None, any strides over tokens
+    and heads; positions int32 [n]; inv_freq float64 [32].  Returns (q_out,
+    k_out or None); q_out may be q, k_out may be k."""
+    _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    _angles(positions, inv_freq, q.shape[0])
+    if k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
+        raise ValueError("q and k must have the same tokens and head dim")
+    hq, q_out = _heads(q, q_weight, q_out, "q", stream)
+    hk = None
+    if k is not None:
+        hk, k_out = _heads(k, k_weight, k_out, "k", stream)
+    _check("mla_qk_norm_rope",
+           load().mla_qk_norm_rope(C.byref(hq), None if hk is None else C.byref(hk), q.shape[0], q.shape[2],
+                                   rope_offset, int(interleaved), float(eps), _ptr(positions), _ptr(inv_freq),
+                                   _stream(stream)))
+    return q_out, (None if k is None else k_out)
+
+
+def mla_kv_norm_rope_append(kv, latent_weight, positions, inv_freq, slot_mapping, kv_pool, num_blocks, block_size,
+                            kv_block_stride, fmt=MLA_KV_NVFP4, eps=1e-6, interleaved=True, q=None, q_weight=None,
+                            rope_offset=0, q_out=None, stream=None):
+    """kv bf16 [n, 576] (latent 512 | key 64): norm of the latent, rotation of
+    the key, quantise-on-write by slot, and q's norm and rotation (as
+    mla_qk_norm_rope) in the same launch.  Returns q_out, or None without q."""
+    _here(kv, latent_weight, positions, inv_freq, slot_mapping, kv_pool, q, q_weight if q is not None else None, q_out)
+    if kv.dtype != torch.bfloat16:
+        raise TypeError(f"kv: expected torch.bfloat16, got {kv.dtype}")
+    if kv.dim() != 2 or kv.shape[1] != 576 or (kv.numel() > 0 and kv.stride(1) != 1):
+        raise ValueError("kv must be [n, 576] with a contiguous last axis")
+    n = kv.shape[0]
+    if _contig(latent_weight, torch.bfloat16, "latent_weight").numel() != 512:
+        raise ValueError("latent_weight must have 512 values")
+    if _contig(slot_mapping, torch.int64, "slot_mapping").numel() != n:
+        raise ValueError(f"slot_mapping must have one entry for each of {n} tokens")
+    _angles(positions, inv_freq, n)
+    _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt)
+    hq = None
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n:
+            raise ValueError("q must be [n, heads, dim] for the tokens of kv")
+        hq, q_out = _heads(q, q_weight, q_out, "q", stream)
+    _check("mla_kv_norm_rope_append",
+           load().mla_kv_norm_rope_append(_ptr(kv), kv.stride(0), _ptr(latent_weight),
+                                          None if hq is None else C.byref(hq), 0 if q is None else q.shape[2],
+                                          rope_offset, int(interleaved), float(eps), _ptr(positions),
+                                          _ptr(inv_freq), _ptr(slot_mapping), n, _ptr(kv_pool), num_blocks,
+                                          block_size, kv_block_stride, fmt, _stream(stream)))
+    return None if q is None else q_out
+
+
+def _dense_tensors(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size,
+                   out, lse, workspace, stream):
+    """Checks what the two dense decodes share; returns (q_nope, q_rope, batch, q_len, heads, out)."""
+    q_nope = _bits(q_nope, "q_nope")
+    q_rope = _bits(q_rope, "q_rope")
+    _contig(block_table, torch.int32, "block_table")
+    _contig(context_lens, torch.int32, "context_lens")
+    dev = _here(q_nope, q_rope, kv_pool, block_table, context_lens, out, lse, workspace)
+    if q_nope.dim() != 4 or q_nope.shape[3] != 512 or tuple(q_rope.shape) != (*q_nope.shape[:3], 64):
+        raise ValueError("q_nope must be [B, Q, H, 512] and q_rope [B, Q, H, 64]")
+    batch, q_len, heads = q_nope.shape[:3]
+    if block_table.dim() != 2 or block_table.shape[0] != batch or context_lens.numel() != batch:
+        raise ValueError("block_table [B, W] and context_lens [B] must fit q_nope [B, Q, H, 512]")
+    _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt)
+    out = _take(out, (batch, q_len, heads, 512), torch.bfloat16, "out", dev, stream)
+    if lse is not None:
+        _take(lse, (batch, q_len, heads), torch.float32, "lse", dev, stream)
+    return q_nope, q_rope, batch, q_len, heads, out
+
+
+def mla_window_decode_workspace_size(batch: int, q_len: int, num_heads: int, max_blocks_per_req: int, sinks: int,
+                                     window: int) -> int:
+    return int(load().mla_window_decode_workspace_size(batch, q_len, num_heads, max_blocks_per_req, sinks, window))
+
+
+def mla_window_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, softmax_scale,
+                      sinks, window, fmt=MLA_KV_NVFP4, block_size=64, out=None, lse=None, workspace=None,
+                      stream=None):
+    """Every query token sees the first `sinks` positions and the last `window`
+    up to its own.  q_nope [B,Q,H,512], q_rope [B,Q,H,64], the Q tokens the last
+    positions of context_lens.  Returns (out bf16 [B,Q,H,512], lse or None)."""
+    q_nope, q_rope, batch, q_len, heads, out = _dense_tensors(
+        q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
+        workspace, stream)
+    if workspace is None:
+        need = mla_window_decode_workspace_size(batch, q_len, heads, block_table.shape[1], sinks, window)
+        workspace = _new((need,), torch.uint8, out.device, stream) if need > 0 else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("mla_window_decode",
+           load().mla_window_decode(_ptr(q_nope), _ptr(q_rope), _ptr(kv_pool), kv_block_stride, num_blocks,
+                                    _ptr(block_table), block_table.shape[1], _ptr(context_lens), batch, q_len, heads,
+                                    block_size, sinks, window, float(softmax_scale), fmt, _ptr(out), _ptr(lse),
+                                    _ptr(workspace), ws_bytes, _stream(stream)))
+    return out, lse
+
+
+def mla_prefix_decode_workspace_size(batch: int, q_len: int, num_heads: int, prefix_len: int,
+                                     max_blocks_per_req: int, max_context_len: int) -> int:
+    return int(load().mla_prefix_decode_workspace_size(batch, q_len, num_heads, prefix_len, max_blocks_per_req,
+                                                       max_context_len))
+
+
+def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, prefix_table, prefix_len, block_table,
+                      context_lens, softmax_scale, max_context_len, fmt=MLA_KV_NVFP4, block_size=64, out=None,
+                      lse=None, workspace=None, stream=None):
+    """Every query token sees the `prefix_len` rows of prefix_table and its own
+    request's rows up to itself.  q_nope [B,Q,H,512], q_rope [B,Q,H,64];
+    context_lens counts the tokens after the prefix, at most max_context_len.
+    Returns (out bf16 [B,Q,H,512], lse or None)."""
+    q_nope, q_rope, batch, q_len, heads, out = _dense_tensors(
+        q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
+        workspace, stream)
+    if prefix_len > 0:
+        _here(out, prefix_table)
+        if _contig(prefix_table, torch.int32, "prefix_table").numel() * block_size < prefix_len:
+            raise ValueError("prefix_table does not reach prefix_len")
+    if workspace is None:
+        need = mla_prefix_decode_workspace_size(batch, q_len, heads, prefix_len, block_table.shape[1],
+                                                max_context_len)
+        workspace = _new((need,), torch.uint8, out.device, stream) if need > 0 else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("mla_prefix_decode",
+           load().mla_prefix_decode(_ptr(q_nope), _ptr(q_rope), _ptr(kv_pool), kv_block_stride, num_blocks,
+                                    _ptr(prefix_table), prefix_len, _ptr(block_table), block_table.shape[1],
+                                    _ptr(context_lens), batch, q_len, heads, block_size, max_context_len,
+                                    float(softmax_scale), fmt, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                                    _stream(stream)))
+    return out, lse

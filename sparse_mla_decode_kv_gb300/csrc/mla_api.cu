@@ -84,6 +84,82 @@ mla_status_t decode_impl(int fmt, const uint16_t* q_nope, const uint16_t* q_rope
                                           softmax_scale, out, lse, workspace, plan, stream));
 }
 
+constexpr int kMaxWindow = 0x7FFFFF00;  // a wider window sees everything a 32-bit context can hold
+
+mla_status_t check_dense_args(const uint16_t* q_nope, const uint16_t* q_rope, const void* kv_pool,
+                              int64_t kv_block_stride, int64_t num_blocks, const int32_t* block_table,
+                              int max_blocks_per_req, const int32_t* context_lens, int batch, int q_len,
+                              int num_heads, int block_size, float softmax_scale, int fmt, const uint16_t* out,
+                              const float* lse) {
+  if (fmt != MLA_KV_NVFP4 && fmt != MLA_KV_FP8) return MLA_ERR_INVALID_ARG;
+  if (q_len < 1 || q_len > kMaxQueryTokens) return MLA_ERR_INVALID_ARG;
+  // the list pointer's place is taken by the table: these decodes have no list
+  mla_status_t s = check_decode_args(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table,
+                                     max_blocks_per_req, context_lens, block_table, batch, num_heads, block_size, 1,
+                                     softmax_scale, out, fmt);
+  if (s != MLA_OK || batch == 0) return s;
+  if (!aligned(q_rope, 16) || (lse && !aligned(lse, 4))) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(batch) * q_len * num_heads > 0x7FFFFFFF) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+int64_t window_rows(int q_len, int max_blocks_per_req, int sinks, int window) {
+  const int64_t held = static_cast<int64_t>(max_blocks_per_req) * kBlock;
+  const int64_t seen = static_cast<int64_t>(sinks) + window + q_len - 1;
+  return seen < held ? seen : held;
+}
+int64_t own_rows(int max_blocks_per_req, int max_context_len) {
+  const int64_t held = static_cast<int64_t>(max_blocks_per_req) * kBlock;
+  return max_context_len < held ? max_context_len : held;
+}
+mla_status_t run_dense(int fmt, const DenseArgs& a, const DensePlan& plan, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  if (plan.workspace > 0) {
+    if (workspace_bytes < plan.workspace) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  }
+  return cuda_status(launch_dense_decode(fmt, a, plan, workspace, stream));
+}
+
+mla_status_t check_heads(const mla_heads_t* h, int64_t n_tokens, int head_dim) {
+  if (h->heads < 0) return MLA_ERR_INVALID_ARG;
+  if (h->heads == 0 || n_tokens == 0) return MLA_OK;
+  if (!h->in || !h->out || !aligned(h->in, 16) || !aligned(h->out, 16)) return MLA_ERR_INVALID_ARG;
+  if (h->weight && !aligned(h->weight, 16)) return MLA_ERR_INVALID_ARG;
+  if (h->in_token_stride % 8 || h->in_head_stride % 8 || h->out_token_stride % 8 || h->out_head_stride % 8)
+    return MLA_ERR_INVALID_ARG;
+  // two rows of the output must not be one
+  if (n_tokens > 1 && h->out_token_stride < head_dim) return MLA_ERR_INVALID_ARG;
+  if (h->heads > 1 && h->out_head_stride < head_dim) return MLA_ERR_INVALID_ARG;
+  if (h->in == h->out && ((n_tokens > 1 && h->in_token_stride != h->out_token_stride) ||
+                          (h->heads > 1 && h->in_head_stride != h->out_head_stride)))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+HeadSet head_set(const mla_heads_t* h) {
+  if (h == nullptr || h->heads == 0) return HeadSet{};
+  return HeadSet{h->in,           h->out, h->heads, h->in_token_stride, h->in_head_stride, h->out_token_stride,
+                 h->out_head_stride, h->weight};
+}
+mla_status_t check_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t n_tokens, int head_dim,
+                             int rope_offset, float eps, const int32_t* positions, const double* inv_freq) {
+  if (n_tokens < 0 || !(eps > 0.f) || !std::isfinite(eps)) return MLA_ERR_INVALID_ARG;
+  if (q || k) {
+    if (head_dim < kRope || head_dim % 8 != 0 || rope_offset < 0 || rope_offset % 8 != 0 ||
+        rope_offset > head_dim - kRope)
+      return MLA_ERR_INVALID_ARG;
+    if (head_dim > 256) return MLA_ERR_UNSUPPORTED;
+  }
+  for (const mla_heads_t* h : {q, k}) {
+    if (h == nullptr) continue;
+    const mla_status_t s = check_heads(h, n_tokens, head_dim);
+    if (s != MLA_OK) return s;
+  }
+  if (n_tokens == 0) return MLA_OK;
+  if (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 8)) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -476,6 +552,173 @@ mla_status_t mla_indexer_topk(const uint16_t* q_idx, const float* head_w, const 
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_topk(scores, max_context_len, context_lens, batch, topk, max_context_len, topk_out,
                                  ws ? ws + scores_bytes : nullptr, st));
+}
+
+mla_status_t mla_block_table_extend(const int32_t* context_lens, const int32_t* new_lens, int batch,
+                                    int32_t* block_table, int max_blocks_per_req, const int32_t* free_blocks,
+                                    int64_t free_capacity, const int64_t* free_state, int64_t num_blocks,
+                                    int block_size, int64_t* slot_mapping, int32_t* positions, int64_t num_slots,
+                                    int32_t* query_start, int32_t* context_lens_out, int64_t* free_state_out,
+                                    mla_stream_t stream) {
+  if (batch < 0 || max_blocks_per_req < 1 || free_capacity < 0 || num_blocks < 0 || num_slots < 0)
+    return MLA_ERR_INVALID_ARG;
+  mla_status_t s = check_block_size(block_size);
+  if (s != MLA_OK) return s;
+  if (num_slots > 0x7FFFFFFF) return MLA_ERR_INVALID_ARG;  // starts are 32-bit
+  if (batch > 0 && (!context_lens || !new_lens || !block_table || !context_lens_out)) return MLA_ERR_INVALID_ARG;
+  if (num_slots > 0 && (!slot_mapping || !positions)) return MLA_ERR_INVALID_ARG;
+  if (!free_state || !free_state_out || !query_start || (free_capacity > 0 && !free_blocks))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) ||
+      !aligned(free_state, 8) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(query_start, 4) ||
+      !aligned(context_lens_out, 4) || !aligned(free_state_out, 8))
+    return MLA_ERR_INVALID_ARG;
+  const ExtendArgs a{context_lens,  new_lens,   batch,        block_table, max_blocks_per_req,
+                     free_blocks,   free_capacity, free_state, num_blocks,  slot_mapping,
+                     positions,     num_slots,  query_start,  context_lens_out, free_state_out};
+  return cuda_status(launch_block_table_extend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_qk_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t n_tokens, int head_dim,
+                              int rope_offset, int interleaved, float eps, const int32_t* positions,
+                              const double* inv_freq, mla_stream_t stream) {
+  if (!q && !k) return MLA_ERR_INVALID_ARG;
+  mla_status_t s = check_norm_rope(q, k, n_tokens, head_dim, rope_offset, eps, positions, inv_freq);
+  if (s != MLA_OK || n_tokens == 0) return s;
+  NormRopeArgs a{};
+  a.set[0] = head_set(q);
+  a.set[1] = head_set(k);
+  a.tokens = n_tokens;
+  a.dim = head_dim;
+  a.rope_offset = rope_offset;
+  a.eps = eps;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.interleaved = interleaved != 0;
+  return cuda_status(launch_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_kv_norm_rope_append(const uint16_t* kv, int64_t kv_token_stride, const uint16_t* latent_weight,
+                                     const mla_heads_t* q, int head_dim, int rope_offset, int interleaved, float eps,
+                                     const int32_t* positions, const double* inv_freq, const int64_t* slot_mapping,
+                                     int64_t n_tokens, void* kv_pool, int64_t num_blocks, int block_size,
+                                     int64_t kv_block_stride, mla_kv_format_t fmt, mla_stream_t stream) {
+  if (num_blocks < 0 || (fmt != MLA_KV_NVFP4 && fmt != MLA_KV_FP8)) return MLA_ERR_INVALID_ARG;
+  mla_status_t s = check_block_size(block_size);
+  if (s != MLA_OK) return s;
+  if (kv_block_stride % 16 != 0 || kv_block_stride < static_cast<int64_t>(block_size) * row_bytes(fmt))
+    return MLA_ERR_INVALID_ARG;
+  s = check_norm_rope(q, nullptr, n_tokens, head_dim, rope_offset, eps, positions, inv_freq);
+  if (s != MLA_OK || n_tokens == 0) return s;
+  if (!kv || !latent_weight || !slot_mapping || !kv_pool) return MLA_ERR_INVALID_ARG;
+  if (!aligned(kv, 16) || !aligned(latent_weight, 16) || !aligned(slot_mapping, 8) || !aligned(kv_pool, 16) ||
+      kv_token_stride % 8 != 0)
+    return MLA_ERR_INVALID_ARG;
+  NormRopeArgs a{};
+  a.set[0] = head_set(q);
+  a.tokens = n_tokens;
+  a.dim = q ? head_dim : kRope;
+  a.rope_offset = rope_offset;
+  a.eps = eps;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.interleaved = interleaved != 0;
+  a.kv = kv;
+  a.kv_token = kv_token_stride;
+  a.latent_weight = latent_weight;
+  a.slot_mapping = slot_mapping;
+  a.pool = static_cast<uint8_t*>(kv_pool);
+  a.num_blocks = num_blocks;
+  a.block_stride = kv_block_stride;
+  a.fmt = fmt;
+  return cuda_status(launch_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_window_decode_workspace_size(int batch, int q_len, int num_heads, int max_blocks_per_req, int sinks,
+                                        int window) {
+  if (batch <= 0 || q_len < 1 || num_heads < 16 || num_heads % 16 != 0 || max_blocks_per_req < 1 || sinks < 0 ||
+      window < 1)
+    return 0;
+  return plan_dense_decode(batch, q_len, num_heads, window_rows(q_len, max_blocks_per_req, sinks, window), 0).workspace;
+}
+
+mla_status_t mla_window_decode(const uint16_t* q_nope, const uint16_t* q_rope, const void* kv_pool,
+                               int64_t kv_block_stride, int64_t num_blocks, const int32_t* block_table,
+                               int max_blocks_per_req, const int32_t* context_lens, int batch, int q_len,
+                               int num_heads, int block_size, int sinks, int window, float softmax_scale,
+                               mla_kv_format_t fmt, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes, mla_stream_t stream) {
+  if (sinks < 0 || window < 1) return MLA_ERR_INVALID_ARG;
+  mla_status_t s = check_dense_args(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table,
+                                    max_blocks_per_req, context_lens, batch, q_len, num_heads, block_size,
+                                    softmax_scale, fmt, out, lse);
+  if (s != MLA_OK || batch == 0) return s;
+  DenseArgs a{};
+  a.q_nope = q_nope;
+  a.q_rope = q_rope;
+  a.pool = static_cast<const uint8_t*>(kv_pool);
+  a.block_stride = kv_block_stride;
+  a.num_blocks = num_blocks;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks_per_req;
+  a.ctx_lens = context_lens;
+  a.max_context = 0x7FFFFFFF;
+  a.batch = batch;
+  a.q_len = q_len;
+  a.num_heads = num_heads;
+  a.sinks = sinks;
+  a.window = window < kMaxWindow ? window : kMaxWindow;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  const DensePlan plan =
+      plan_dense_decode(batch, q_len, num_heads, window_rows(q_len, max_blocks_per_req, sinks, window), 0);
+  return run_dense(fmt, a, plan, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t mla_prefix_decode_workspace_size(int batch, int q_len, int num_heads, int prefix_len, int max_blocks_per_req,
+                                        int max_context_len) {
+  if (batch <= 0 || q_len < 1 || num_heads < 16 || num_heads % 16 != 0 || prefix_len < 0 || max_blocks_per_req < 1 ||
+      max_context_len < 0)
+    return 0;
+  return plan_dense_decode(batch, q_len, num_heads, own_rows(max_blocks_per_req, max_context_len), prefix_len).workspace;
+}
+
+mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, const void* kv_pool,
+                               int64_t kv_block_stride, int64_t num_blocks, const int32_t* prefix_table,
+                               int prefix_len, const int32_t* block_table, int max_blocks_per_req,
+                               const int32_t* context_lens, int batch, int q_len, int num_heads, int block_size,
+                               int max_context_len, float softmax_scale, mla_kv_format_t fmt, uint16_t* out,
+                               float* lse, void* workspace, size_t workspace_bytes, mla_stream_t stream) {
+  if (prefix_len < 0 || prefix_len > kMaxWindow || max_context_len < 0) return MLA_ERR_INVALID_ARG;
+  mla_status_t s = check_dense_args(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table,
+                                    max_blocks_per_req, context_lens, batch, q_len, num_heads, block_size,
+                                    softmax_scale, fmt, out, lse);
+  if (s != MLA_OK || batch == 0) return s;
+  if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4))) return MLA_ERR_INVALID_ARG;
+  DenseArgs a{};
+  a.q_nope = q_nope;
+  a.q_rope = q_rope;
+  a.pool = static_cast<const uint8_t*>(kv_pool);
+  a.block_stride = kv_block_stride;
+  a.num_blocks = num_blocks;
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks_per_req;
+  a.ctx_lens = context_lens;
+  a.max_context = max_context_len;
+  a.batch = batch;
+  a.q_len = q_len;
+  a.num_heads = num_heads;
+  a.sinks = 0;
+  a.window = kMaxWindow;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  const DensePlan plan =
+      plan_dense_decode(batch, q_len, num_heads, own_rows(max_blocks_per_req, max_context_len), prefix_len);
+  return run_dense(fmt, a, plan, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace mla {
@@ -89,6 +90,93 @@ bool sparse_decode_tc_supported(int fmt, int num_heads);
 bool sparse_decode_uses_tc(int fmt, int num_heads, int64_t block_stride, int64_t num_blocks);
 int plan_sparse_decode_tc(int pairs, int num_heads, int topk, int max_splits);
 cudaError_t launch_sparse_decode_tc(const TcDecodeParams& p, const CUtensorMap& map, cudaStream_t stream);
+
+// Dense decode over a window and / or a shared prefix (dense_decode.cu).
+struct DensePlan {
+  int groups_per_req;  // 64-column groups of a request's (query token, head) pairs
+  int splits;          // CTAs per group along its own rows
+  int prefix_groups;   // 64-column groups of the whole batch over the prefix (0 without one)
+  int prefix_splits;   // CTAs per such group along the prefix
+  size_t workspace;    // bytes of partials, 0 for a single slice
+};
+struct DenseArgs {
+  const uint16_t* q_nope;
+  const uint16_t* q_rope;
+  const uint8_t* pool;
+  int64_t block_stride;
+  int64_t num_blocks;
+  const int32_t* prefix_table;
+  int prefix_len;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* ctx_lens;
+  int max_context;  // longer contexts are cut to it
+  int batch;
+  int q_len;
+  int num_heads;
+  int sinks;
+  int window;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  // set by the launch from the plan
+  int groups_per_req, splits, prefix_groups, prefix_splits, parts;
+  int64_t columns;
+  __half* part_o;
+  float* part_lse;
+  unsigned int* fault_word;
+};
+DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_rows, int prefix_len);
+cudaError_t launch_dense_decode(int fmt, DenseArgs a, const DensePlan& plan, void* workspace, cudaStream_t stream);
+
+// Block tables and slot maps from request lengths (block_table.cu).
+struct ExtendArgs {
+  const int32_t* context_lens;
+  const int32_t* new_lens;
+  int batch;
+  int32_t* block_table;
+  int max_blocks;
+  const int32_t* free_blocks;
+  int64_t free_capacity;
+  const int64_t* free_state;
+  int64_t num_blocks;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int64_t num_slots;
+  int32_t* query_start;
+  int32_t* context_lens_out;
+  int64_t* free_state_out;
+};
+cudaError_t launch_block_table_extend(const ExtendArgs& a, cudaStream_t stream);
+
+// Norms and rotation of query / key heads and of latent rows (norm_rope.cu).
+struct HeadSet {  // bf16 heads [tokens, heads, dim], the last axis contiguous; null = none
+  const uint16_t* in;
+  uint16_t* out;
+  int heads;
+  int64_t in_token, in_head, out_token, out_head;  // strides in elements
+  const uint16_t* weight;                          // bf16 [dim], or null: no norm
+};
+struct NormRopeArgs {
+  HeadSet set[2];  // queries, keys
+  int64_t tokens;
+  int dim;
+  int rope_offset;
+  float eps;
+  const int32_t* positions;
+  const double* inv_freq;  // [32]
+  bool interleaved;
+  // latent rows into the cache
+  const uint16_t* kv;  // bf16 [tokens, 576], or null
+  int64_t kv_token;    // stride in elements
+  const uint16_t* latent_weight;
+  const int64_t* slot_mapping;
+  uint8_t* pool;
+  int64_t num_blocks;
+  int64_t block_stride;
+  int fmt;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 
 // Indexer and top-k.
 size_t topk_workspace_bytes(int batch, int max_context_len, int topk);

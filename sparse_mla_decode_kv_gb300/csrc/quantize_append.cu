@@ -22,19 +22,6 @@ namespace {
 
 constexpr int kWarpsPerBlock = 8;
 
-// x / d (d > 0) rounded to nearest-even, i.e. the IEEE float32 quotient,
-// from the correctly rounded reciprocal and one FMA correction step
-// (Markstein's theorem: with r = RN(1/d) and q0 = RN(x r),
-// RN(q0 + RN(x - q0 d) r) = RN(x/d) while quotient and residual stay in the
-// normal range).  Tiny quotients (x subnormal) round to 0 in both e2m1 and
-// e4m3 whichever way their last bit goes.  The correction turns -0 into +0,
-// so the quotient takes x's sign explicitly.
-__device__ __forceinline__ float div_rn(float x, float d, float r) {
-  const float q0 = __fmul_rn(x, r);
-  const float e = __fmaf_rn(-q0, d, x);
-  return copysignf(__fmaf_rn(e, r, q0), x);
-}
-
 template <int FMT>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     quantize_append_kernel(const uint16_t* __restrict__ latent, const uint16_t* __restrict__ rope,
@@ -76,34 +63,9 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
       const uint32_t rope_e4m3x2 =
           f32x2_to_e4m3x2(bf16_bits_to_f32(rope2[u] >> 16), bf16_bits_to_f32(rope2[u] & 0xFFFFu));
 
-      if constexpr (FMT == 0) {
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-        // S = e4m3(amax / 6): IEEE division, then round-to-nearest-even.
-        const uint32_t s_code = f32x2_to_e4m3x2(0.f, __fdiv_rn(amax, 6.0f)) & 0xFFu;
-        const uint32_t s_f16 = e4m3x2_to_f16x2(s_code) & 0xFFFFu;
-        const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(s_f16)));
-        uint32_t lo = 0, hi = 0;  // 16 codes: element 2i in the low nibble of byte i
-        if (s_code != 0) {
-          const float r = __frcp_rn(s);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo |= f32x2_to_e2m1x2(div_rn(x[2 * i + 1], s, r), div_rn(x[2 * i], s, r)) << (8 * i);
-            hi |= f32x2_to_e2m1x2(div_rn(x[8 + 2 * i + 1], s, r), div_rn(x[8 + 2 * i], s, r)) << (8 * i);
-          }
-        }
-        *reinterpret_cast<uint2*>(row + lane * 8) = make_uint2(lo, hi);
-        row[kScaleOff + lane] = static_cast<uint8_t>(s_code);
-        *reinterpret_cast<uint16_t*>(row + kRopeOffNvfp4 + 2 * lane) = static_cast<uint16_t>(rope_e4m3x2);
-      } else {
-        uint32_t b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[i] = f32x2_to_e4m3x2(x[4 * i + 1], x[4 * i]) | (f32x2_to_e4m3x2(x[4 * i + 3], x[4 * i + 2]) << 16);
-        *reinterpret_cast<uint4*>(row + lane * 16) = make_uint4(b[0], b[1], b[2], b[3]);
-        *reinterpret_cast<uint16_t*>(row + kRopeOffFp8 + 2 * lane) = static_cast<uint16_t>(rope_e4m3x2);
-      }
+      store_latent_row<FMT>(row, lane, x);
+      *reinterpret_cast<uint16_t*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 2 * lane) =
+          static_cast<uint16_t>(rope_e4m3x2);
     }
   }
 }
