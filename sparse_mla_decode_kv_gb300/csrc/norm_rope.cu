@@ -33,7 +33,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kPairs = kRope / 2;
-constexpr int kHeadsPerTask = 4;  // consecutive (token, head) rows of one lane group, loaded together
+constexpr int kKvCtasPerSm = 6;
+constexpr int kHeadsPerTask = 4;  // consecutive (token, head) rows of one lane group
 
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -42,152 +43,240 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 __device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
 // sin and cos of position x the pair's frequency (a 64-bit fraction of a turn).
+// The nearest quarter turn is split off as an integer, so that the float holds
+// an eighth of a turn at most (its rounding is 2^-27 of a turn, not 2^-25).
 __device__ __forceinline__ void angle(uint64_t turn, int position, float* s, float* c) {
   const uint64_t phase = turn * static_cast<uint64_t>(static_cast<int64_t>(position));
-  sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, s, c);  // 2^-31
+  const uint32_t hi = static_cast<uint32_t>(phase >> 32);
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
+  float sn, cs;
+  sincospif(static_cast<float>(static_cast<int32_t>(hi - (quarter << 30))) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+  const float x = (quarter & 1) ? cs : sn, y = (quarter & 1) ? sn : cs;
+  *s = (quarter & 2) ? -x : x;
+  *c = ((quarter + 1) & 2) ? -y : y;
 }
 
-// One lane group (G lanes, 8 values each) per run of heads.
-template <int G>
+// Two floats at a time (the packed forms issue once for both).
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{ .reg .b64 p, q; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %5}; mul.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{ .reg .b64 p, q, r; mov.b64 p, {%2, %3}; mov.b64 q, {%4, %5}; mov.b64 r, {%6, %7}; "
+      "fma.rn.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ F2 bf16x2_floats(uint32_t two) {
+  return {__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u)};
+}
+
+// Eight lanes per head: lane l of them has the 8-value chunks l, l + 8, ... (C
+// at most), 128 contiguous bytes a load.  The rotated part is 8 consecutive
+// chunks, so every lane has exactly one of them, chunk (l - offset / 8) % 8 of
+// the part, and half-split pairs lie in lanes l and l ^ 4.  A lane group takes
+// kHeadsPerTask consecutive (token, head) rows: the angles of a token are
+// computed once for up to that many of its heads, and 4 heads share each
+// instruction.
+template <int C>
 __device__ __forceinline__ void norm_rope_heads(const NormRopeArgs& a, const HeadSet& hs, int64_t task,
                                                 const uint64_t* turns) {
-  const int lane = threadIdx.x & 31;
-  const int gl = lane & (G - 1);
+  const int gl = threadIdx.x & 7;
   const int64_t rows = a.tokens * hs.heads;
   const int64_t r0 = task * kHeadsPerTask;
-  const bool has = 8 * gl < a.dim;
-  const int rc = gl - a.rope_offset / 8;  // 8-value chunk within the rotated part
-  const bool turned = rc >= 0 && rc < kRope / 8;
-  uint4 x[kHeadsPerTask];
-  int64_t tok[kHeadsPerTask];
-  int head[kHeadsPerTask];
-  tok[0] = rows <= 0x7FFFFFFF ? static_cast<uint32_t>(r0) / static_cast<uint32_t>(hs.heads) : r0 / hs.heads;
-  head[0] = static_cast<int>(r0 - tok[0] * hs.heads);
+  const int chunks = a.dim / 8;
+  const int off = a.rope_offset / 8;
+  const int rc = (gl - off) & 7;              // this lane's chunk within the rotated part
+  const int c_rope = (off + rc - gl) / 8;     // and among its own
+  F2 w[C][4];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerTask; ++i) {
-    if (i > 0) {
-      const bool wrap = head[i - 1] + 1 == hs.heads;
-      tok[i] = tok[i - 1] + wrap;
-      head[i] = wrap ? 0 : head[i - 1] + 1;
-    }
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (has && r0 + i < rows)
-      x[i] = *reinterpret_cast<const uint4*>(hs.in + tok[i] * hs.in_token + head[i] * hs.in_head + 8 * gl);
+  for (int c = 0; c < C; ++c) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (hs.weight != nullptr && gl + 8 * c < chunks) v = __ldg(reinterpret_cast<const uint4*>(hs.weight) + gl + 8 * c);
+    w[c][0] = bf16x2_floats(v.x);
+    w[c][1] = bf16x2_floats(v.y);
+    w[c][2] = bf16x2_floats(v.z);
+    w[c][3] = bf16x2_floats(v.w);
   }
-  uint4 w4 = make_uint4(0, 0, 0, 0);
-  if (has && hs.weight != nullptr) w4 = __ldg(reinterpret_cast<const uint4*>(hs.weight) + gl);
-  const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
-  int64_t angle_tok = -1;
-  // interleaved: this chunk's pairs; else half of them, the other half is the partner's
-  float sn[4] = {0.f, 0.f, 0.f, 0.f}, cs[4] = {0.f, 0.f, 0.f, 0.f};
+  int64_t tok = rows <= 0x7FFFFFFF ? static_cast<uint32_t>(r0) / static_cast<uint32_t>(hs.heads) : r0 / hs.heads;
+  int head = static_cast<int>(r0 - tok * hs.heads);
+  const uint16_t* in = hs.in + tok * hs.in_token + head * hs.in_head + 8 * gl;
+  uint16_t* out = hs.out + tok * hs.out_token + head * hs.out_head + 8 * gl;
+  const int64_t in_wrap = hs.in_token - (hs.heads - 1) * hs.in_head;
+  const int64_t out_wrap = hs.out_token - (hs.heads - 1) * hs.out_head;
+  uint4 next[C];
+  auto load = [&](bool in_range) {
 #pragma unroll
+    for (int c = 0; c < C; ++c)
+      next[c] = in_range && gl + 8 * c < chunks ? *reinterpret_cast<const uint4*>(in + 64 * c) : make_uint4(0, 0, 0, 0);
+  };
+  load(r0 < rows);
+  const float inv_dim = 1.f / static_cast<float>(a.dim);
+  bool fresh = true;  // the angles are another token's
+  float sn[4], cs[4];  // interleaved: this chunk's pairs; else half of them, the other half is the partner's
+#pragma unroll 1
   for (int i = 0; i < kHeadsPerTask; ++i) {
-    const bool in = r0 + i < rows;  // uniform over the lane group
-    const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float v[8];
+    const bool here = r0 + i < rows;  // uniform over the lane group
+    F2 v[C][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = bf16_bits_to_f32(xw[k] & 0xFFFFu);
-      v[2 * k + 1] = __uint_as_float(xw[k] & 0xFFFF0000u);
+    for (int c = 0; c < C; ++c) {
+      v[c][0] = bf16x2_floats(next[c].x);
+      v[c][1] = bf16x2_floats(next[c].y);
+      v[c][2] = bf16x2_floats(next[c].z);
+      v[c][3] = bf16x2_floats(next[c].w);
     }
+    const int64_t now = tok;
+    const bool first = fresh;
+    uint16_t* const dst = out;
+    const bool wrap = ++head == hs.heads;
+    in += wrap ? in_wrap : hs.in_head;
+    out += wrap ? out_wrap : hs.out_head;
+    head = wrap ? 0 : head;
+    tok += wrap;
+    fresh = wrap;
+    if (i + 1 < kHeadsPerTask) load(r0 + i + 1 < rows);
     if (hs.weight != nullptr) {
-      float ss = 0.f;
+      F2 ss = {0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int off = G / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-      const float rstd = rsqrtf(ss / static_cast<float>(a.dim) + a.eps);
+        for (int k = 0; k < 4; ++k) ss = fma2(v[c][k], v[c][k], ss);
+      float s = ss.x + ss.y;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] *= rstd * bf16_bits_to_f32(ww[k] & 0xFFFFu);
-        v[2 * k + 1] *= rstd * __uint_as_float(ww[k] & 0xFFFF0000u);
-      }
+      for (int m = 4; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+      const float rstd = rsqrtf(s * inv_dim + a.eps);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[c][k] = mul2(mul2(v[c][k], F2{rstd, rstd}), w[c][k]);
     }
-    if (turned && in && tok[i] != angle_tok) {
-      angle_tok = tok[i];
-      const int pos = __ldg(a.positions + angle_tok);
+    if (first && here) {
+      const int pos = __ldg(a.positions + now);
       const int p0 = a.interleaved ? 4 * rc : 8 * (rc & 3) + (rc & 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) angle(turns[p0 + k], pos, &sn[k], &cs[k]);
     }
+    F2 r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r[k] = v[0][k];
+#pragma unroll
+      for (int c = 1; c < C; ++c) r[k] = c_rope == c ? v[c][k] : r[k];
+    }
     if (a.interleaved) {
-      if (turned) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float p = v[2 * k], q = v[2 * k + 1];
-          v[2 * k] = p * cs[k] - q * sn[k];
-          v[2 * k + 1] = q * cs[k] + p * sn[k];
-        }
-      }
+      for (int k = 0; k < 4; ++k) r[k] = {r[k].x * cs[k] - r[k].y * sn[k], r[k].y * cs[k] + r[k].x * sn[k]};
     } else {
-      // chunk rc and its partner rc ^ 4 hold the two halves of 8 pairs and
-      // half of their angles each
-      const int src = turned ? lane + ((rc & 4) ? -4 : 4) : lane;
-      const float sign = (rc & 4) ? 1.f : -1.f;
+      // chunk rc and its partner rc ^ 4 hold the two halves of 8 pairs and half
+      // of their angles each
+      const bool upper = (rc & 4) != 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float other = __shfl_sync(0xFFFFFFFFu, v[k], src);
-        const float so = __shfl_sync(0xFFFFFFFFu, sn[k & 3], src), co = __shfl_sync(0xFFFFFFFFu, cs[k & 3], src);
-        const bool mine = (k >> 2) == ((rc >> 2) & 1);
-        const float s = mine ? sn[k & 3] : so, c = mine ? cs[k & 3] : co;
-        if (turned) v[k] = v[k] * c + sign * other * s;
+      for (int k = 0; k < 4; ++k) {
+        const float ox = __shfl_xor_sync(0xFFFFFFFFu, r[k].x, 4), oy = __shfl_xor_sync(0xFFFFFFFFu, r[k].y, 4);
+        const int e = 2 * (k & 1);  // values 2 k, 2 k + 1: pairs of the lower or the upper four
+        const float s0 = __shfl_xor_sync(0xFFFFFFFFu, sn[e], 4), s1 = __shfl_xor_sync(0xFFFFFFFFu, sn[e + 1], 4);
+        const float c0 = __shfl_xor_sync(0xFFFFFFFFu, cs[e], 4), c1 = __shfl_xor_sync(0xFFFFFFFFu, cs[e + 1], 4);
+        const bool mine = (k >= 2) == upper;
+        const float sx = mine ? sn[e] : s0, sy = mine ? sn[e + 1] : s1;
+        const float cx = mine ? cs[e] : c0, cy = mine ? cs[e + 1] : c1;
+        r[k] = {r[k].x * cx + (upper ? ox : -ox) * sx, r[k].y * cy + (upper ? oy : -oy) * sy};
       }
     }
-    if (has && in)
-      *reinterpret_cast<uint4*>(hs.out + tok[i] * hs.out_token + head[i] * hs.out_head + 8 * gl) =
-          make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[c][k] = c_rope == c ? r[k] : v[c][k];
+      if (here && gl + 8 * c < chunks)
+        *reinterpret_cast<uint4*>(dst + 64 * c) =
+            make_uint4(bf16x2_rn(v[c][0].x, v[c][0].y), bf16x2_rn(v[c][1].x, v[c][1].y),
+                       bf16x2_rn(v[c][2].x, v[c][2].y), bf16x2_rn(v[c][3].x, v[c][3].y));
+    }
   }
 }
 
 // One warp per latent row: lane g owns scale group g (16 latent values) and
-// one rotated pair.
+// one rotated pair.  A warp strides over rows and has two in flight: the next
+// row's loads are issued before this one's arithmetic.  Weights and the pair's
+// frequency stay in registers.
+struct LatentRow {
+  int64_t slot;
+  uint4 v0, v1;
+  uint32_t p, q;
+  int pos;
+};
 template <int FMT>
-__device__ __forceinline__ void norm_rope_append_row(const NormRopeArgs& a, int64_t n, const uint64_t* turns) {
+__device__ __forceinline__ void norm_rope_append_rows(const NormRopeArgs& a, int64_t first, int64_t stride,
+                                                      const uint64_t* turns) {
   const int lane = threadIdx.x & 31;
-  const int64_t slot = __ldg(a.slot_mapping + n);
-  const uint16_t* src = a.kv + n * a.kv_token;
-  const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src + lane * kGroup));
-  const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src + lane * kGroup) + 1);
-  const int e0 = a.interleaved ? 2 * lane : lane, e1 = a.interleaved ? 2 * lane + 1 : lane + kPairs;
-  const float p = bf16_bits_to_f32(__ldg(src + kLatent + e0)), q = bf16_bits_to_f32(__ldg(src + kLatent + e1));
-  const int pos = __ldg(a.positions + n);
   const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(a.latent_weight + lane * kGroup));
   const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(a.latent_weight + lane * kGroup) + 1);
-  if (slot < 0 || slot / kBlock >= a.num_blocks) return;  // skipped (warp-uniform)
-  const uint32_t xw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  float x[16], ss = 0.f;
+  const uint64_t turn = turns[lane];
+  const int e0 = a.interleaved ? 2 * lane : lane, e1 = a.interleaved ? 2 * lane + 1 : lane + kPairs;
+  auto load = [&](int64_t n) {
+    LatentRow r;
+    r.slot = -1;
+    if (n < a.tokens) {
+      r.slot = __ldg(a.slot_mapping + n);
+      const uint16_t* src = a.kv + n * a.kv_token;
+      r.v0 = __ldg(reinterpret_cast<const uint4*>(src + lane * kGroup));
+      r.v1 = __ldg(reinterpret_cast<const uint4*>(src + lane * kGroup) + 1);
+      r.p = __ldg(src + kLatent + e0);
+      r.q = __ldg(src + kLatent + e1);
+      r.pos = __ldg(a.positions + n);
+    }
+    return r;
+  };
+  LatentRow next = load(first);
+  for (int64_t n = first; n < a.tokens; n += stride) {
+    const LatentRow r = next;
+    next = load(n + stride);
+    if (r.slot < 0 || r.slot / kBlock >= a.num_blocks) continue;  // skipped (warp-uniform)
+    const uint32_t xw[8] = {r.v0.x, r.v0.y, r.v0.z, r.v0.w, r.v1.x, r.v1.y, r.v1.z, r.v1.w};
+    float x[16], ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = bf16_bits_to_f32(xw[i] & 0xFFFFu);
-    x[2 * i + 1] = __uint_as_float(xw[i] & 0xFFFF0000u);
-    ss = fmaf(x[2 * i], x[2 * i], ss);
-    ss = fmaf(x[2 * i + 1], x[2 * i + 1], ss);
-  }
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = bf16_bits_to_f32(xw[i] & 0xFFFFu);
+      x[2 * i + 1] = __uint_as_float(xw[i] & 0xFFFF0000u);
+      ss = fmaf(x[2 * i], x[2 * i], ss);
+      ss = fmaf(x[2 * i + 1], x[2 * i + 1], ss);
+    }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-  const float rstd = rsqrtf(ss * (1.f / kLatent) + a.eps);
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+    const float rstd = rsqrtf(ss * (1.f / kLatent) + a.eps);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = bf16_rn(x[2 * i] * (rstd * bf16_bits_to_f32(ww[i] & 0xFFFFu)));
-    x[2 * i + 1] = bf16_rn(x[2 * i + 1] * (rstd * __uint_as_float(ww[i] & 0xFFFF0000u)));
-  }
-  float s, c;
-  angle(turns[lane], pos, &s, &c);
-  const uint32_t rope2 = f32x2_to_e4m3x2(bf16_rn(q * c + p * s), bf16_rn(p * c - q * s));
-  uint8_t* row = a.pool + (slot / kBlock) * a.block_stride + (slot % kBlock) * (FMT == 0 ? kRowNvfp4 : kRowFp8);
-  store_latent_row<FMT>(row, lane, x);
-  uint8_t* rope = row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8);
-  if (a.interleaved) {
-    *reinterpret_cast<uint16_t*>(rope + 2 * lane) = static_cast<uint16_t>(rope2);
-  } else {
-    rope[lane] = static_cast<uint8_t>(rope2);
-    rope[lane + kPairs] = static_cast<uint8_t>(rope2 >> 8);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t two = bf16x2_rn(x[2 * i] * (rstd * bf16_bits_to_f32(ww[i] & 0xFFFFu)),
+                                     x[2 * i + 1] * (rstd * __uint_as_float(ww[i] & 0xFFFF0000u)));
+      x[2 * i] = bf16_bits_to_f32(two & 0xFFFFu);
+      x[2 * i + 1] = __uint_as_float(two & 0xFFFF0000u);
+    }
+    float s, c;
+    angle(turn, r.pos, &s, &c);
+    const float p = bf16_bits_to_f32(r.p), q = bf16_bits_to_f32(r.q);
+    const uint32_t rope2 = f32x2_to_e4m3x2(bf16_rn(q * c + p * s), bf16_rn(p * c - q * s));
+    uint8_t* row = a.pool + (r.slot / kBlock) * a.block_stride + (r.slot % kBlock) * (FMT == 0 ? kRowNvfp4 : kRowFp8);
+    store_latent_row<FMT>(row, lane, x);
+    uint8_t* rope = row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8);
+    if (a.interleaved) {
+      *reinterpret_cast<uint16_t*>(rope + 2 * lane) = static_cast<uint16_t>(rope2);
+    } else {
+      rope[lane] = static_cast<uint8_t>(rope2);
+      rope[lane + kPairs] = static_cast<uint8_t>(rope2 >> 8);
+    }
   }
 }
 
 // CTAs [0, kv_ctas) take latent rows, the others tasks of the two head sets.
-template <int G>
+template <int C, int FMT>
 __global__ void __launch_bounds__(kWarps * 32)
     norm_rope_kernel(const NormRopeArgs a, unsigned kv_ctas, int64_t q_tasks, int64_t tasks) {
   __shared__ uint64_t turns[kPairs];
@@ -197,44 +286,56 @@ __global__ void __launch_bounds__(kWarps * 32)
     turns[threadIdx.x] = static_cast<uint64_t>((f - floor(f)) * 18446744073709551616.0);
   }
   __syncthreads();
-  if (blockIdx.x < kv_ctas) {
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (n >= a.tokens) return;
-    if (a.fmt == 0)
-      norm_rope_append_row<0>(a, n, turns);
-    else
-      norm_rope_append_row<1>(a, n, turns);
+  if (FMT >= 0 && blockIdx.x < kv_ctas) {
+    norm_rope_append_rows<FMT>(a, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+                               static_cast<int64_t>(kv_ctas) * kWarps, turns);
     return;
   }
-  const int64_t task = (static_cast<int64_t>(blockIdx.x - kv_ctas) * (kWarps * 32) + threadIdx.x) / G;
-  // whole warps stay together: the shuffles name every lane
-  const int64_t warp_first = (static_cast<int64_t>(blockIdx.x - kv_ctas) * (kWarps * 32) + (threadIdx.x & ~31u)) / G;
-  if (warp_first >= tasks) return;
-  // q_tasks is a multiple of the tasks per warp, so a warp has one set
-  const bool is_k = warp_first >= q_tasks;
-  norm_rope_heads<G>(a, a.set[is_k], task - (is_k ? q_tasks : 0), turns);
+  if constexpr (C > 0) {
+    const int64_t cta = static_cast<int64_t>(blockIdx.x - kv_ctas);
+    const int64_t task = (cta * (kWarps * 32) + threadIdx.x) / 8;
+    // whole warps stay together: the shuffles name every lane
+    const int64_t warp_first = (cta * (kWarps * 32) + (threadIdx.x & ~31u)) / 8;
+    if (warp_first >= tasks) return;
+    // q_tasks is a multiple of the tasks per warp, so a warp has one set
+    const bool is_k = warp_first >= q_tasks;
+    norm_rope_heads<C>(a, a.set[is_k], task - (is_k ? q_tasks : 0), turns);
+  }
+}
+
+template <int C>
+cudaError_t launch_chunks(const NormRopeArgs& a, unsigned grid, unsigned kv_ctas, int64_t q_tasks, int64_t tasks,
+                         cudaStream_t stream) {
+  auto* kernel = a.kv == nullptr ? norm_rope_kernel<C, -1> : a.fmt == 0 ? norm_rope_kernel<C, 0> : norm_rope_kernel<C, 1>;
+  kernel<<<grid, kWarps * 32, 0, stream>>>(a, kv_ctas, q_tasks, tasks);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  const int group = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;  // lanes per head, 8 values each
-  const int per_warp = 32 / group;
   int64_t set_tasks[2];
   for (int i = 0; i < 2; ++i) {
     const int64_t rows = a.set[i].in != nullptr ? a.tokens * a.set[i].heads : 0;
-    const int64_t t = (rows + kHeadsPerTask - 1) / kHeadsPerTask;
-    set_tasks[i] = (t + per_warp - 1) / per_warp * per_warp;
+    set_tasks[i] = ((rows + kHeadsPerTask - 1) / kHeadsPerTask + 3) / 4 * 4;  // whole warps
   }
   const int64_t tasks = set_tasks[0] + set_tasks[1];
-  const int64_t kv_ctas = a.kv != nullptr ? (a.tokens + kWarps - 1) / kWarps : 0;
-  const int64_t head_ctas = (tasks * group + kWarps * 32 - 1) / (kWarps * 32);
+  // latent rows: at most kKvCtasPerSm CTAs per SM, whose warps stride over them
+  const int64_t kv_want = a.kv != nullptr ? (a.tokens + kWarps - 1) / kWarps : 0;
+  const int64_t kv_cap = static_cast<int64_t>(device_sm_count()) * kKvCtasPerSm;
+  const int64_t kv_ctas = kv_want < kv_cap ? kv_want : kv_cap;
+  const int64_t head_ctas = (tasks * 8 + kWarps * 32 - 1) / (kWarps * 32);
   const int64_t grid = kv_ctas + head_ctas;
   if (grid == 0) return cudaSuccess;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  auto* kernel = group == 8 ? norm_rope_kernel<8> : group == 16 ? norm_rope_kernel<16> : norm_rope_kernel<32>;
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a, static_cast<unsigned>(kv_ctas), set_tasks[0], tasks);
-  return cudaGetLastError();
+  const unsigned g = static_cast<unsigned>(grid), k = static_cast<unsigned>(kv_ctas);
+  switch (tasks == 0 ? 0 : (a.dim + 63) / 64) {  // 8-value chunks per lane
+    case 0: return launch_chunks<0>(a, g, k, set_tasks[0], tasks, stream);
+    case 1: return launch_chunks<1>(a, g, k, set_tasks[0], tasks, stream);
+    case 2: return launch_chunks<2>(a, g, k, set_tasks[0], tasks, stream);
+    case 3: return launch_chunks<3>(a, g, k, set_tasks[0], tasks, stream);
+    default: return launch_chunks<4>(a, g, k, set_tasks[0], tasks, stream);
+  }
 }
 
 }  // namespace mla
