@@ -407,39 +407,51 @@ def mla_indexer_topk(q_idx, head_w, idx_key_pool, idx_block_stride, num_blocks, 
 
 
 # --------------------------------------------------------------------- block tables, norms, dense decodes
-def _here(*tensors) -> torch.device:
+# These calls are also made for single tokens, where the host's share is most of
+# the time: devices are compared as numbers, addresses passed as numbers, and
+# the current stream read without a stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(*tensors) -> int:
     """The one device of `tensors` (None left out), which has to be the current one."""
-    device = None
+    device = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        device = device or t.device
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    if device is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but cuda:{torch.cuda.current_device()} is the current device")
+        if t is not None and t.get_device() != device:
+            if not t.is_cuda:
+                raise ValueError("expected a CUDA tensor")
+            raise ValueError(f"a tensor on {t.device}, but cuda:{device} is the current device")
     return device
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """Memory whose reuse is ordered behind the stream the call runs on."""
+def _on(stream, device: int) -> int:
+    """The address of `stream`, or of the device's current one."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _new(like, shape, dtype, stream) -> torch.Tensor:
+    """Memory on `like`'s device whose reuse is ordered behind the stream the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype) if dtype is not like.dtype else like.new_empty(shape)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _take(t, shape, dtype, name, device, stream) -> torch.Tensor:
+def _take(t, shape, dtype, name, like, stream) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
-        return _new(shape, dtype, device, stream)
-    if tuple(t.shape) != tuple(shape):
+        return _new(like, shape, dtype, stream)
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return _contig(t, dtype, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt) -> None:
@@ -461,23 +473,23 @@ def mla_block_table_extend(context_lens, new_lens, block_table, free_blocks, fre
     block_table = _contig(block_table, torch.int32, "block_table")
     free_blocks = _contig(free_blocks, torch.int32, "free_blocks")
     free_state = _contig(free_state, torch.int64, "free_state")
-    dev = _here(context_lens, new_lens, block_table, free_blocks, free_state, slot_mapping, positions, query_start,
-                context_lens_out, free_state_out)
+    device = _here(context_lens, new_lens, block_table, free_blocks, free_state, slot_mapping, positions, query_start,
+                   context_lens_out, free_state_out)
     batch = context_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != batch or new_lens.numel() != batch or \
             free_state.numel() != 3:
         raise ValueError("new_lens [B], block_table [B, W] and free_state [3] must fit context_lens [B]")
-    slot_mapping = _take(slot_mapping, (num_slots,), torch.int64, "slot_mapping", dev, stream)
-    positions = _take(positions, (num_slots,), torch.int32, "positions", dev, stream)
-    query_start = _take(query_start, (batch + 1,), torch.int32, "query_start", dev, stream)
-    context_lens_out = _take(context_lens_out, (batch,), torch.int32, "context_lens_out", dev, stream)
-    free_state_out = _take(free_state_out, (3,), torch.int64, "free_state_out", dev, stream)
+    slot_mapping = _take(slot_mapping, (num_slots,), torch.int64, "slot_mapping", free_state, stream)
+    positions = _take(positions, (num_slots,), torch.int32, "positions", context_lens, stream)
+    query_start = _take(query_start, (batch + 1,), torch.int32, "query_start", context_lens, stream)
+    context_lens_out = _take(context_lens_out, (batch,), torch.int32, "context_lens_out", context_lens, stream)
+    free_state_out = _take(free_state_out, (3,), torch.int64, "free_state_out", free_state, stream)
     _check("mla_block_table_extend",
-           load().mla_block_table_extend(_ptr(context_lens), _ptr(new_lens), batch, _ptr(block_table),
-                                         block_table.shape[1], _ptr(free_blocks), free_blocks.numel(),
-                                         _ptr(free_state), num_blocks, block_size, _ptr(slot_mapping),
-                                         _ptr(positions), num_slots, _ptr(query_start), _ptr(context_lens_out),
-                                         _ptr(free_state_out), _stream(stream)))
+           load().mla_block_table_extend(_at(context_lens), _at(new_lens), batch, _at(block_table),
+                                         block_table.shape[1], _at(free_blocks), free_blocks.numel(), _at(free_state),
+                                         num_blocks, block_size, _at(slot_mapping), _at(positions), num_slots,
+                                         _at(query_start), _at(context_lens_out), _at(free_state_out),
+                                         _on(stream, device)))
     return slot_mapping, positions, query_start, context_lens_out, free_state_out
 
 
@@ -493,7 +505,7 @@ def _heads(x, weight, out, name, stream):
     if weight is not None and _contig(weight, torch.bfloat16, name + "_weight").numel() != x.shape[2]:
         raise ValueError(f"{name}_weight must have one value for each of {x.shape[2]} dims")
     if out is None:
-        out = _new(x.shape, torch.bfloat16, x.device, stream)
+        out = _new(x, x.shape, torch.bfloat16, stream)
     return _Heads(x.data_ptr(), out.data_ptr(), x.shape[1], x.stride(0), x.stride(1), out.stride(0), out.stride(1),
                   None if weight is None else weight.data_ptr()), out
 
@@ -511,7 +523,7 @@ def mla_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     on.  q bf16 [n, Hq, D], k bf16 [n, Hk, D] or None, any strides over tokens
     and heads; positions int32 [n]; inv_freq float64 [32].  Returns (q_out,
     k_out or None); q_out may be q, k_out may be k."""
-    _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    device = _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     _angles(positions, inv_freq, q.shape[0])
     if k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
         raise ValueError("q and k must have the same tokens and head dim")
@@ -521,8 +533,8 @@ def mla_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
         hk, k_out = _heads(k, k_weight, k_out, "k", stream)
     _check("mla_qk_norm_rope",
            load().mla_qk_norm_rope(C.byref(hq), None if hk is None else C.byref(hk), q.shape[0], q.shape[2],
-                                   rope_offset, int(interleaved), float(eps), _ptr(positions), _ptr(inv_freq),
-                                   _stream(stream)))
+                                   rope_offset, int(interleaved), float(eps), _at(positions), _at(inv_freq),
+                                   _on(stream, device)))
     return q_out, (None if k is None else k_out)
 
 
@@ -532,7 +544,8 @@ def mla_kv_norm_rope_append(kv, latent_weight, positions, inv_freq, slot_mapping
     """kv bf16 [n, 576] (latent 512 | key 64): norm of the latent, rotation of
     the key, quantise-on-write by slot, and q's norm and rotation (as
     mla_qk_norm_rope) in the same launch.  Returns q_out, or None without q."""
-    _here(kv, latent_weight, positions, inv_freq, slot_mapping, kv_pool, q, q_weight if q is not None else None, q_out)
+    device = _here(kv, latent_weight, positions, inv_freq, slot_mapping, kv_pool, q,
+                   q_weight if q is not None else None, q_out)
     if kv.dtype != torch.bfloat16:
         raise TypeError(f"kv: expected torch.bfloat16, got {kv.dtype}")
     if kv.dim() != 2 or kv.shape[1] != 576 or (kv.numel() > 0 and kv.stride(1) != 1):
@@ -550,32 +563,32 @@ def mla_kv_norm_rope_append(kv, latent_weight, positions, inv_freq, slot_mapping
             raise ValueError("q must be [n, heads, dim] for the tokens of kv")
         hq, q_out = _heads(q, q_weight, q_out, "q", stream)
     _check("mla_kv_norm_rope_append",
-           load().mla_kv_norm_rope_append(_ptr(kv), kv.stride(0), _ptr(latent_weight),
+           load().mla_kv_norm_rope_append(_at(kv), kv.stride(0), _at(latent_weight),
                                           None if hq is None else C.byref(hq), 0 if q is None else q.shape[2],
-                                          rope_offset, int(interleaved), float(eps), _ptr(positions),
-                                          _ptr(inv_freq), _ptr(slot_mapping), n, _ptr(kv_pool), num_blocks,
-                                          block_size, kv_block_stride, fmt, _stream(stream)))
+                                          rope_offset, int(interleaved), float(eps), _at(positions), _at(inv_freq),
+                                          _at(slot_mapping), n, _at(kv_pool), num_blocks, block_size,
+                                          kv_block_stride, fmt, _on(stream, device)))
     return None if q is None else q_out
 
 
 def _dense_tensors(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size,
                    out, lse, workspace, stream):
-    """Checks what the two dense decodes share; returns (q_nope, q_rope, batch, q_len, heads, out)."""
+    """Checks what the two dense decodes share; returns (q_nope, q_rope, batch, q_len, heads, out, device)."""
     q_nope = _bits(q_nope, "q_nope")
     q_rope = _bits(q_rope, "q_rope")
     _contig(block_table, torch.int32, "block_table")
     _contig(context_lens, torch.int32, "context_lens")
-    dev = _here(q_nope, q_rope, kv_pool, block_table, context_lens, out, lse, workspace)
+    device = _here(q_nope, q_rope, kv_pool, block_table, context_lens, out, lse, workspace)
     if q_nope.dim() != 4 or q_nope.shape[3] != 512 or tuple(q_rope.shape) != (*q_nope.shape[:3], 64):
         raise ValueError("q_nope must be [B, Q, H, 512] and q_rope [B, Q, H, 64]")
     batch, q_len, heads = q_nope.shape[:3]
     if block_table.dim() != 2 or block_table.shape[0] != batch or context_lens.numel() != batch:
         raise ValueError("block_table [B, W] and context_lens [B] must fit q_nope [B, Q, H, 512]")
     _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt)
-    out = _take(out, (batch, q_len, heads, 512), torch.bfloat16, "out", dev, stream)
+    out = _take(out, (batch, q_len, heads, 512), torch.bfloat16, "out", q_nope, stream)
     if lse is not None:
-        _take(lse, (batch, q_len, heads), torch.float32, "lse", dev, stream)
-    return q_nope, q_rope, batch, q_len, heads, out
+        _take(lse, (batch, q_len, heads), torch.float32, "lse", q_nope, stream)
+    return q_nope, q_rope, batch, q_len, heads, out, device
 
 
 def mla_window_decode_workspace_size(batch: int, q_len: int, num_heads: int, max_blocks_per_req: int, sinks: int,
@@ -589,18 +602,18 @@ def mla_window_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, bloc
     """Every query token sees the first `sinks` positions and the last `window`
     up to its own.  q_nope [B,Q,H,512], q_rope [B,Q,H,64], the Q tokens the last
     positions of context_lens.  Returns (out bf16 [B,Q,H,512], lse or None)."""
-    q_nope, q_rope, batch, q_len, heads, out = _dense_tensors(
+    q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
     if workspace is None:
         need = mla_window_decode_workspace_size(batch, q_len, heads, block_table.shape[1], sinks, window)
-        workspace = _new((need,), torch.uint8, out.device, stream) if need > 0 else None
+        workspace = _new(kv_pool, (need,), torch.uint8, stream) if need > 0 else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("mla_window_decode",
-           load().mla_window_decode(_ptr(q_nope), _ptr(q_rope), _ptr(kv_pool), kv_block_stride, num_blocks,
-                                    _ptr(block_table), block_table.shape[1], _ptr(context_lens), batch, q_len, heads,
-                                    block_size, sinks, window, float(softmax_scale), fmt, _ptr(out), _ptr(lse),
-                                    _ptr(workspace), ws_bytes, _stream(stream)))
+           load().mla_window_decode(_at(q_nope), _at(q_rope), _at(kv_pool), kv_block_stride, num_blocks,
+                                    _at(block_table), block_table.shape[1], _at(context_lens), batch, q_len, heads,
+                                    block_size, sinks, window, float(softmax_scale), fmt, _at(out), _at(lse),
+                                    _at(workspace), ws_bytes, _on(stream, device)))
     return out, lse
 
 
@@ -617,7 +630,7 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
     request's rows up to itself.  q_nope [B,Q,H,512], q_rope [B,Q,H,64];
     context_lens counts the tokens after the prefix, at most max_context_len.
     Returns (out bf16 [B,Q,H,512], lse or None)."""
-    q_nope, q_rope, batch, q_len, heads, out = _dense_tensors(
+    q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
     if prefix_len > 0:
@@ -627,12 +640,12 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
     if workspace is None:
         need = mla_prefix_decode_workspace_size(batch, q_len, heads, prefix_len, block_table.shape[1],
                                                 max_context_len)
-        workspace = _new((need,), torch.uint8, out.device, stream) if need > 0 else None
+        workspace = _new(kv_pool, (need,), torch.uint8, stream) if need > 0 else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("mla_prefix_decode",
-           load().mla_prefix_decode(_ptr(q_nope), _ptr(q_rope), _ptr(kv_pool), kv_block_stride, num_blocks,
-                                    _ptr(prefix_table), prefix_len, _ptr(block_table), block_table.shape[1],
-                                    _ptr(context_lens), batch, q_len, heads, block_size, max_context_len,
-                                    float(softmax_scale), fmt, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-                                    _stream(stream)))
+           load().mla_prefix_decode(_at(q_nope), _at(q_rope), _at(kv_pool), kv_block_stride, num_blocks,
+                                    _at(prefix_table), prefix_len, _at(block_table), block_table.shape[1],
+                                    _at(context_lens), batch, q_len, heads, block_size, max_context_len,
+                                    float(softmax_scale), fmt, _at(out), _at(lse), _at(workspace), ws_bytes,
+                                    _on(stream, device)))
     return out, lse
