@@ -3,28 +3,31 @@
 // requests share a prefix.  NVFP4 or FP8 rows, f16 operands, f32 accumulation.
 //
 // Mathematics.  64 "columns" -- (query token, head) pairs that look at the
-// same cached rows -- share one walk over those rows, a cache block of 64 rows
-// (one tile) at a time:
-//   S[64 rows x 64 columns] = K[64 x 576] . Q^T
+// same cached rows -- share one walk over those rows, half a cache block of 32
+// rows (one tile) at a time:
+//   S[64 columns x 32 rows] = Q[64 x 576] . K^T
 //   P = 2^(S scale - m), m the column's running maximum (raised lazily)
-//   O^T[512 x 64] = O^T + V^T[512 x 64] . P,   V = the first 512 of K
+//   O^T[512 x 64] = O^T + V^T[512 x 32] . P^T,   V = the first 512 of K
 // and each column's denominator is summed in float beside it, so the rows are
 // read and unpacked once for all 64 columns.  A request's query tokens and
 // heads fill columns; where the rows are a shared prefix, so do the requests.
 //
-// Work split.  One CTA = 64 columns x a slice of their blocks; slices' partial
+// Work split.  One CTA = 64 columns x a slice of their tiles; slices' partial
 // outputs (normalised, f16) and base-2 LSEs are joined by dense_merge_kernel.
-// Roles: one lane issues every tcgen05.mma; one copies each block, which is
-// contiguous, with one bulk copy into one of two slots; 8 warps unpack; 8 run
-// the softmax; all 16 write the output.  The unpacked tile is stored once, as
-// 8 x 8 core matrices, dim group major, which is at the same time the K-major A
-// operand of S (M = 64 rows) and the MN-major A operand of O^T (M = 128 dims).
-// It is handed over in five pieces (rope, 4 x 128 latent dims) through a ring
-// that fills what shared memory the query and the block slots leave: two rope
-// pieces and 4 (FP8, 64 columns) to 8 (NVFP4, 16 columns) latent ones.  A
-// latent piece is refilled as soon as the O^T product has left it; with the
-// pieces beyond a tile's own the next tile's unpacking and its part of S run
-// during the softmax.  P lies in the tile's rope piece, which only S reads.
+// Roles: one lane issues every tcgen05.mma; one copies each tile, which is
+// contiguous, with one bulk copy; two sets of 4 warps unpack tiles in turn; 4
+// warps run the softmax, 16 columns each; all write the output.  The unpacked
+// tile is stored once, as 8 x 8 core matrices, dim group major, which is at the
+// same time the K-major B operand of S (N = 32 rows) and the MN-major A operand
+// of O^T (M = 128 dims).  P lies in the tile's rope part, which only S reads.
+//
+// What bounds it.  Both products read their operands from shared memory at its
+// full rate (S: 36 MMAs of ~24 cycles, O^T: 8 of ~48 per tile), and each tile
+// is a chain of hand-offs -- copy, unpack, S, softmax, O^T -- of several hundred
+// cycles each.  What hides the chain is tiles in flight: S of the next tile is
+// issued before O^T of this one.  32 rows and not 64 or 128, so that three
+// unpacked tiles (37 KB each) fit beside a 72 KB query; at 64 rows only pieces
+// of the next tile did.
 //
 // Every wait is bounded; one that runs out sets the library's fault bit and
 // the CTA leaves after its copies and MMAs in flight have drained.
@@ -41,17 +44,18 @@
 namespace mla {
 namespace {
 
-constexpr int kRows = kBlock;  // rows per tile: one cache block
-constexpr int kCols = 64;      // columns per CTA
+constexpr int kRows = 32;  // rows per tile: half a cache block
+constexpr int kCols = 64;  // columns per CTA
 // Warp 0 issues the MMAs (a warp's instructions wait for those of older warps
 // on its scheduler: as the youngest, it issued one MMA in ~200 cycles), warp 1
 // copies, then the unpack and the softmax warps.
 constexpr int kMmaWarp = 0;
 constexpr int kCopyWarp = 1;
 constexpr int kFirstUnpack = 2;
-constexpr int kUnpackWarps = 8;
+constexpr int kUnpackSet = 4;  // warps that unpack one tile, 8 rows each
+constexpr int kUnpackWarps = 2 * kUnpackSet;
 constexpr int kFirstSoftmax = kFirstUnpack + kUnpackWarps;
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 4;  // one per tensor-memory quadrant
 constexpr int kWarps = kUnpackWarps + kSoftmaxWarps;
 constexpr int kComputeThreads = kWarps * 32;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -59,46 +63,50 @@ constexpr int kThreads = kComputeThreads + 32 * kFirstUnpack;
 constexpr int kDimGroups = (kLatent + kRope) / 8;  // 72
 // One 8-dim group of a tile: 16 bytes a row and 16 bytes of padding, see
 // RawPiece.
-constexpr int kDgBytes = kRows * 16 + 16;       // 1,040
-constexpr int kLatPiece = 16 * kDgBytes;        // 128 latent dims: 16,640
-constexpr int kRopePiece = 8 * kDgBytes;        // 64 rope dims, or P: 8,320
-constexpr int kQGroupBytes = kDimGroups * 128;  // 8 columns x 576 dims: 9,216
-constexpr int kMaxSlots = 2;
-constexpr int kMaxPieces = 8;
+constexpr int kDgBytes = kRows * 16 + 16;             // 528
+constexpr int kTileBytes = kDimGroups * kDgBytes;     // 38,016
+constexpr int kPOff = kLatent / 8 * kDgBytes;         // P overlays the rope part
+constexpr int kPGroupBytes = kRows / 8 * 128;         // P of 8 columns: 512
+constexpr int kQGroupBytes = kDimGroups * 128;        // 8 columns x 576 dims: 9,216
+constexpr int kMaxSlots = 4;                          // copied tiles
+constexpr int kMaxTiles = 4;                          // unpacked tiles
+static_assert(kCols / 8 * kPGroupBytes <= kRope / 8 * kDgBytes, "P fits the rope part");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOCol = 128;  // S: columns 0-63 and 64-127 (tiles in turn), O^T: 128-383
+constexpr uint32_t kOCol = 64;  // S: columns 0-31 and 32-63 (tiles in turn), O^T: 64-319
 // The maximum of a column is raised only when a score exceeds it by 2^8: P
 // stays within 2^8 in f16 and O^T is rarely rescaled.
 constexpr float kLazyRaise = 8.f;
-constexpr int kPolls = 1 << 16;  // of the MMA warp, while it may do either of two things
 constexpr float kLn2f = 0.6931471805599453f;
 
-struct Ctl {               // the fixed part of shared memory, at its start
-  float red[kSoftmaxWarps][32];  // per warp, per column reduction scratch
-  float m_ref[kCols];      // running (lazy) maximum, base 2
-  float alpha[kCols];      // factor of the last raise; at the end 1 / denominator
-  float qscale[kCols];     // softmax scale (base 2) x 2^-shift of the column's query
-  uint32_t qmax[kCols];    // largest |q| of the column (bf16 magnitude bits)
-  uint64_t raw_full[kMaxSlots], raw_free[kMaxSlots];
-  uint64_t rope_full[2], rope_free[2], full[kMaxPieces], free_[kMaxPieces];
-  uint64_t s_full, p_full, done;
+struct Ctl {              // the fixed part of shared memory, at its start
+  float alpha[kCols];     // factor of the last raise; at the end 1 / denominator
+  float qscale[kCols];    // softmax scale (base 2) x 2^-shift of the column's query
+  uint32_t qmax[kCols];   // largest |q| of the column (bf16 magnitude bits)
+  // raw_full: tile n's is the (n % (2 slots))-th, so that each has waiters of one
+  // unpack set only, which see all its phases even where the slots are three.
+  uint64_t raw_full[2 * kMaxSlots], raw_free[kMaxSlots], full[kMaxTiles], free_[kMaxTiles];
+  uint64_t s_full[2], p_full[2], o_done[2], done;
   uint32_t tmem_base;
   int abort_flag;  // set by whoever ran out of polls; ends the others' waits
   int abort_tile;  // first tile whose barrier a softmax warp reached with a failed wait
 };
-constexpr int kCtlBytes = 4096;
+constexpr int kNoAbort = 0x7FFFFFFF;
+constexpr int kCtlBytes = 2048;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int row_bytes(int fmt) { return fmt == 0 ? kRowNvfp4 : kRowFp8; }
-// Latent pieces that fit beside the rest for a CTA of `cols` columns, and block
-// slots: two where that leaves a piece beyond a tile's own, else one.
-__host__ __device__ constexpr int latent_pieces(int fmt, int cols, int slots) {
-  const int left = kSmemBytes - kCtlBytes - slots * kRows * row_bytes(fmt) - cols / 8 * kQGroupBytes - 2 * kRopePiece;
-  return left / kLatPiece < kMaxPieces ? left / kLatPiece : kMaxPieces;
+// Unpacked and copied tiles that fit beside the query of `cols` columns: first
+// two copies, then unpacked tiles, then more copies.
+__host__ __device__ constexpr int tile_room(int cols) { return kSmemBytes - kCtlBytes - cols / 8 * kQGroupBytes; }
+__host__ __device__ constexpr int unpacked_tiles(int fmt, int cols) {
+  const int n = (tile_room(cols) - 2 * kRows * row_bytes(fmt)) / kTileBytes;
+  return n < kMaxTiles ? n : kMaxTiles;
 }
-__host__ __device__ constexpr int block_slots(int fmt, int cols) { return latent_pieces(fmt, cols, 2) > 4 ? 2 : 1; }
-static_assert(latent_pieces(0, kCols, block_slots(0, kCols)) >= 4 && latent_pieces(1, kCols, block_slots(1, kCols)) >= 4,
-              "a whole tile must fit");
+__host__ __device__ constexpr int copied_tiles(int fmt, int cols) {
+  const int n = (tile_room(cols) - unpacked_tiles(fmt, cols) * kTileBytes) / (kRows * row_bytes(fmt));
+  return n < kMaxSlots ? n : kMaxSlots;
+}
+static_assert(unpacked_tiles(0, kCols) >= 3 && unpacked_tiles(1, kCols) >= 3, "three tiles in flight");
 
 // ---- tcgen05 operands ---------------------------------------------------------
 // No-swizzle shared-memory descriptor, in two words: start and byte offset
@@ -147,8 +155,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 16 lanes x 32 columns of this warp's quadrant (an M = 64 accumulator's rows
-// 16 quad .. 16 quad + 15) in the matrix-fragment layout: r[4 k + e] is row
+// 16 lanes x 32 columns of this warp's quadrant (rows 16 quad .. 16 quad + 15
+// of an M = 64 accumulator) in the matrix-fragment layout: r[4 k + e] is row
 // lane / 4 + 8 (e / 2), column 8 k + 2 (lane % 4) + e % 2.
 __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -178,15 +186,6 @@ __device__ __noinline__ bool wait_bar_slow(int* abort_flag, uint64_t* bar, uint3
 __device__ __forceinline__ bool wait_bar(int* abort_flag, uint64_t* bar, uint32_t parity, unsigned int* fw) {
   return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_bar_slow(abort_flag, bar, parity, fw);
 }
-__device__ __forceinline__ bool test_bar(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // The same for a whole warp: one lane polls.
 __device__ __forceinline__ bool wait_bar_warp(int* abort_flag, uint64_t* bar, uint32_t parity, unsigned int* fw) {
   bool ok = true;
@@ -202,14 +201,14 @@ __device__ __forceinline__ void warp_publish(uint64_t* bar, int lane) {
 }
 
 // How an unpack warp reads and writes its 8 rows.  The four lanes of a row hold
-// its "quarters": 32 dims of each 128-dim region and 16 rope dims.  Eight
-// lanes (one 16-byte shared-memory access) are two rows, r and r + 2.  Rows are
-// 22 (NVFP4) or 36 (FP8) 16-byte pieces apart: the eight pieces read, 6 r + q
-// (mod 8), fall into different banks; of FP8's two pieces a quarter, row r + 2
-// reads the second first, 4 r + 2 q + h.  Stores go to dim groups 1,040 bytes
-// apart; with quarters 2 and 3 one dim group ahead of 0 and 1, the pieces
-// 4 q + (i + q / 2) % 4 + r (mod 8) differ as well.  Dim group i of a quarter is
-// therefore given as its (i - q / 2)-th, and `ahead` is q / 2; `second` is row r + 2.
+// its "quarters": 32 dims of each 128-dim piece and 16 rope dims.  Eight lanes
+// (one 16-byte shared-memory access) are two rows, r and r + 2.  Rows are 22
+// (NVFP4) or 36 (FP8) 16-byte units apart: the eight units read, 6 r + q (mod
+// 8), fall into different banks; of FP8's two units a quarter, row r + 2 reads
+// the second first, 4 r + 2 q + h.  Stores go to dim groups 528 bytes apart;
+// with quarters 2 and 3 one dim group ahead of 0 and 1, the units 4 q + (i + q /
+// 2) % 4 + r (mod 8) differ as well.  Dim group i of a quarter is therefore
+// given as its (i - q / 2)-th, and `ahead` is q / 2; `second` is row r + 2.
 template <int FMT>
 struct RawPiece;
 template <>
@@ -270,8 +269,8 @@ __device__ __forceinline__ void unpack_rope(const uint4 v, uint32_t (&h)[2][4]) 
 }
 
 // One CTA's work: columns [col0, col0 + ncols) over tiles [begin, end) of a
-// list of cache blocks.  Tile t is logical block t for t < n_sink_blocks, else
-// w_block + t - n_sink_blocks.  Positions in [0, stop) that lie in the first
+// list.  Tile t is the t-th 32 positions for t < n_sink_tiles, else the (w_tile
+// + t - n_sink_tiles)-th.  Positions in [0, stop) that lie in the first
 // `sinks` or from w0 on are seen by some column.
 struct Unit {
   int64_t col0;
@@ -279,7 +278,7 @@ struct Unit {
   int part;  // slot of its partial among a column's
   const int32_t* table;
   int table_len;
-  int n_sink_blocks, w_block, begin, end;
+  int n_sink_tiles, w_tile, begin, end;
   int sinks, w0, stop;
   int tok_col0;  // col0 within its request (own rows)
   int me0;       // position of query token 0 (own rows)
@@ -329,22 +328,23 @@ __device__ __forceinline__ Unit find_unit(const DenseArgs& a) {
     u.sinks = min(a.sinks, u.stop);
     u.w0 = max(u.sinks, me_lo - a.window + 1);
   }
-  u.n_sink_blocks = (u.sinks + kBlock - 1) / kBlock;
-  u.w_block = max(u.w0 / kBlock, u.n_sink_blocks);
-  const int tiles = u.n_sink_blocks + max(0, (u.stop + kBlock - 1) / kBlock - u.w_block);
+  u.n_sink_tiles = (u.sinks + kRows - 1) / kRows;
+  u.w_tile = max(u.w0 / kRows, u.n_sink_tiles);
+  const int tiles = u.n_sink_tiles + max(0, (u.stop + kRows - 1) / kRows - u.w_tile);
   // spread evenly over the splits
   u.begin = static_cast<int>(static_cast<int64_t>(tiles) * sp / splits);
   u.end = static_cast<int>(static_cast<int64_t>(tiles) * (sp + 1) / splits);
   return u;
 }
-__device__ __forceinline__ int tile_block(const Unit& u, int t) {
-  return t < u.n_sink_blocks ? t : u.w_block + (t - u.n_sink_blocks);
+// First position of tile t.
+__device__ __forceinline__ int tile_pos(const Unit& u, int t) {
+  return (t < u.n_sink_tiles ? t : u.w_tile + (t - u.n_sink_tiles)) * kRows;
 }
 // Physical block of tile t as the table has it (it may lie outside the pool),
 // -1 past the slice or the table.
 __device__ __forceinline__ int tile_id(const Unit& u, int t) {
   if (t >= u.end) return -1;
-  const int blk = tile_block(u, t);
+  const int blk = tile_pos(u, t) / kBlock;
   return blk < u.table_len ? __ldg(u.table + blk) : -1;
 }
 
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Ctl& sm = *reinterpret_cast<Ctl*>(smem_raw);
   constexpr int kRowBytes = row_bytes(FMT);
-  constexpr uint32_t kBlockBytes = kRows * kRowBytes;
+  constexpr uint32_t kRawBytes = kRows * kRowBytes;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cw = warp - kFirstUnpack, ct = threadIdx.x - 32 * kFirstUnpack;  // among the unpack and softmax warps
@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Unit u = find_unit(args);
   const int n_tiles = u.end - u.begin;
-  const int n_slots = block_slots(FMT, u.ncols);
-  const int n_pieces = latent_pieces(FMT, u.ncols, n_slots);
-  uint8_t* const s_raw = smem_raw + kCtlBytes;                  // blocks as stored
-  uint8_t* const s_q = s_raw + n_slots * kBlockBytes;           // (col / 8) * 9216 + (dim / 8) * 128 + (col % 8) * 16
-  uint8_t* const s_rope = s_q + u.ncols / 8 * kQGroupBytes;     // (dim / 8) * 1040 + row * 16 + (dim % 8) * 2
-  uint8_t* const s_lat = s_rope + 2 * kRopePiece;               // likewise, 128 dims a piece
+  const int n_slots = copied_tiles(FMT, u.ncols), n_bufs = unpacked_tiles(FMT, u.ncols);
+  // The query comes first: S reads 64 columns of it, of which those past ncols
+  // are whatever follows (rows of S that nobody uses).
+  uint8_t* const s_q = smem_raw + kCtlBytes;                 // (col / 8) * 9216 + (dim / 8) * 128 + (col % 8) * 16
+  uint8_t* const s_tile = s_q + u.ncols / 8 * kQGroupBytes;  // (dim / 8) * 528 + row * 16 + (dim % 8) * 2
+  uint8_t* const s_raw = s_tile + n_bufs * kTileBytes;       // tiles as stored
   const bool direct = args.parts == 1;
   const unsigned pool_blocks = static_cast<unsigned>(min(args.num_blocks, static_cast<int64_t>(0x7FFFFFFF)));
   if (n_tiles <= 0) {  // nothing to see: an empty partial, or the whole answer
@@ -382,28 +382,25 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     }
     return;
   }
-  if (warp >= kFirstUnpack && ct < kCols) {
-    sm.m_ref[ct] = -INFINITY;
-    sm.qmax[ct] = 0;
-  }
+  if (warp >= kFirstUnpack && ct < kCols) sm.qmax[ct] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_free[i], kUnpackWarps);
+      mbar_init(&sm.raw_full[kMaxSlots + i], 1);
+      mbar_init(&sm.raw_free[i], kUnpackSet);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.rope_full[i], kUnpackWarps);
-      mbar_init(&sm.rope_free[i], 1);
-    }
-    for (int i = 0; i < kMaxPieces; ++i) {
-      mbar_init(&sm.full[i], kUnpackWarps);
+    for (int i = 0; i < kMaxTiles; ++i) {
+      mbar_init(&sm.full[i], kUnpackSet);
       mbar_init(&sm.free_[i], 1);
     }
-    mbar_init(&sm.s_full, 1);
-    mbar_init(&sm.p_full, kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kSoftmaxWarps);
+      mbar_init(&sm.o_done[i], 1);
+    }
     mbar_init(&sm.done, 1);
     sm.abort_flag = 0;
-    sm.abort_tile = 0x7FFFFFFF;
+    sm.abort_tile = kNoAbort;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -416,26 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  constexpr uint32_t tbase = 0;  // all 512 columns were allocated: they start at column 0
+  // all 512 tensor-memory columns were allocated: they start at column 0
   int copied = 0;  // copying lane: tiles whose copy it has started
 
-  // The copy of tile n, once its slot is free: one contiguous block, or none
-  // where the table names no block of the pool.
+  // The copy of tile n, once its slot is free: 32 contiguous rows, or none where
+  // the table names no block of the pool.
   auto copy_tile = [&](int n, int id) {
     const int slot = n % n_slots;
     if (n >= n_slots && !wait_bar(&sm.abort_flag, &sm.raw_free[slot], static_cast<uint32_t>(n / n_slots - 1) & 1u, fw))
       return false;
+    uint64_t* const full = &sm.raw_full[n % (2 * n_slots)];
     if (static_cast<unsigned>(id) < pool_blocks) {
-      mbar_expect_tx(&sm.raw_full[slot], kBlockBytes);
-      bulk_load(s_raw + slot * kBlockBytes, args.pool + static_cast<int64_t>(id) * args.block_stride, kBlockBytes,
-                &sm.raw_full[slot]);
+      mbar_expect_tx(full, kRawBytes);
+      bulk_load(s_raw + slot * kRawBytes,
+                args.pool + static_cast<int64_t>(id) * args.block_stride +
+                    tile_pos(u, u.begin + n) % kBlock * kRowBytes,
+                kRawBytes, full);
     } else {
-      mbar_arrive(&sm.raw_full[slot]);
+      mbar_arrive(full);
     }
     copied = n + 1;
     return true;
   };
-  if (warp == kCopyWarp && lane == 0) {  // the first blocks arrive while the query is converted
+  if (warp == kCopyWarp && lane == 0) {  // the first tiles arrive while the query is converted
     for (int n = 0; n < n_slots && n < n_tiles; ++n) copy_tile(n, tile_id(u, u.begin + n));
   }
   if (warp >= kFirstUnpack) {
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     // column whose query holds an infinity or NaN enters as zeros with a NaN
     // scale: its results are NaN, its neighbours' are not.
     constexpr int kPieces = kDimGroups / 4;               // of 32 dims
-    constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 9
+    constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 12
     const int n_tasks = (u.ncols / 8) * kPieces;
     uint4 x[kPer];
 #pragma unroll
@@ -508,89 +508,52 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    // One lane runs the whole role: an MMA piece of 8 then issues in ~190 cycles
-    // (N = 16) to ~260 (N = 64), the tensor core's own rate; a warp-wide loop
-    // with the MMAs behind an election in each turn took 370-410, and rolled
-    // loops, whose operand registers wait for the previous MMA to start, ~800.
-    const uint32_t idesc_s = f16_idesc(64, u.ncols, 0, 0);
-    const uint32_t idesc_o = f16_idesc(128, u.ncols, 1, 1);
-    const uint32_t rope0 = smem_u32(s_rope);
-    const uint32_t q_b = desc_lo(smem_u32(s_q), 128);
-    const uint32_t lat_s = desc_lo(rope0 + 2 * kRopePiece, kDgBytes), rope_s = desc_lo(rope0, kDgBytes);
-    const uint32_t lat_o = desc_lo(rope0 + 2 * kRopePiece, 128), p_o = desc_lo(rope0, 128);
+    // One lane runs the whole role with a tile's MMAs unrolled: they then issue
+    // at the tensor core's own rate (24 cycles at M = 64, N = 32; 40-48 at M =
+    // 128).  A warp-wide loop with an election per piece took twice that, and
+    // rolled loops, whose operand registers wait for the previous MMA to
+    // start, four times.
+    const uint32_t idesc_s = f16_idesc(64, kRows, 0, 0);
+    const uint32_t idesc_o = f16_idesc(128, u.ncols, 1, 0);
+    const uint32_t q_a = desc_lo(smem_u32(s_q), 128);
+    const uint32_t tile_s = desc_lo(smem_u32(s_tile), kDgBytes), tile_o = desc_lo(smem_u32(s_tile), 128);
+    const uint32_t tile_p = desc_lo(smem_u32(s_tile) + kPOff, 128);
     if (elect_one()) {
-      // Ring position of the next S piece and the next O^T piece, as slot, operand
-      // address and (S) phase.
-      int s_slot = 0, o_slot = 0;
-      uint32_t s_a = lat_s, o_a = lat_o, s_phase = 0;
+      int s_buf = 0, o_buf = 0;
+      uint32_t s_phase = 0;
       bool ok = true;
 #pragma unroll 1
-      for (int n = -1; n < n_tiles && ok; ++n) {
-        // S of tile n + 1 piece by piece -- rope (k = 0), then 128 latent dims each
-        // (k = 1..4), 16 dims an MMA -- as its pieces fill, and O^T of tile n as
-        // soon as its P is there.  The last piece of S comes after that: S is
-        // complete only after O^T, so the softmax may rescale O^T, and P of two
-        // tiles is never outstanding.
-        const uint32_t next = static_cast<uint32_t>(n + 1), par = static_cast<uint32_t>(n) & 1u;
-        const int k_end = n + 1 < n_tiles ? 5 : 0;
-        const int k_early = min(k_end, min(4, 1 + n_pieces - 4));  // more cannot be there before O^T
-        bool o_left = n >= 0;
-        int k = 0, polls = 0;
-        uint32_t s_b = q_b;
-#pragma unroll 1
-        while (k < k_end || o_left) {
-          uint64_t* const bar = k == 0 ? &sm.rope_full[next & 1] : &sm.full[s_slot];
-          const uint32_t bar_par = k == 0 ? (next >> 1) & 1u : s_phase;
-          if (o_left && test_bar(&sm.p_full, par)) {
-            tcgen05_fence_after();
-            // O^T += V^T . P, 128 dims at a time, 16 rows an MMA
-            const uint32_t p = p_o + (n & 1) * (kRopePiece >> 4);
+      for (int n = 0; n <= n_tiles && ok; ++n) {
+        if (n < n_tiles) {  // S of tile n, 16 dims an MMA
+          ok = wait_bar(&sm.abort_flag, &sm.full[s_buf], s_phase, fw);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t b = tile_s + s_buf * (kTileBytes >> 4), d = kRows * (n & 1);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll
-              for (int j = 0; j < kRows / 16; ++j)
-                umma_f16<desc_hi(kDgBytes), desc_hi(kDgBytes)>(kOCol + kCols * m, o_a + j * (256 >> 4),
-                                                               p + j * (256 >> 4), idesc_o, n > 0 || j > 0);
-              umma_commit(&sm.free_[o_slot]);
-              if (m == 3) umma_commit(&sm.rope_free[n & 1]);  // P is free when all four are done
-              o_a += kLatPiece >> 4;
-              if (++o_slot == n_pieces) {
-                o_slot = 0;
-                o_a = lat_o;
-              }
-            }
-            o_left = false;
-            polls = 0;
-          } else if (k < (o_left ? k_early : k_end) && test_bar(bar, bar_par)) {
-            tcgen05_fence_after();
-            const uint32_t d = kCols * (next & 1);
-            if (k == 0) {
-              const uint32_t a = rope_s + (next & 1) * (kRopePiece >> 4), b = q_b + kLatent / 8 * (128 >> 4);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_f16<desc_hi(128), desc_hi(kQGroupBytes)>(d, a + 2 * i * (kDgBytes >> 4), b + 2 * i * (128 >> 4),
-                                                              idesc_s, i != 0);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                umma_f16<desc_hi(128), desc_hi(kQGroupBytes)>(d, s_a + 2 * i * (kDgBytes >> 4),
-                                                              s_b + 2 * i * (128 >> 4), idesc_s, true);
-              if (k == 4) umma_commit(&sm.s_full);
-              s_b += 16 * (128 >> 4);
-              s_a += kLatPiece >> 4;
-              if (++s_slot == n_pieces) {
-                s_slot = 0;
-                s_a = lat_s;
-                s_phase ^= 1u;
-              }
-            }
-            ++k;
-            polls = 0;
-          } else if (++polls == kPolls) {  // something is late: a bounded wait for what must come first
-            ok = o_left ? wait_bar(&sm.abort_flag, &sm.p_full, par, fw) : wait_bar(&sm.abort_flag, bar, bar_par, fw);
-            if (!ok) break;
-            polls = 0;
+          for (int i = 0; i < kDimGroups / 2; ++i)
+            umma_f16<desc_hi(kQGroupBytes), desc_hi(128)>(d, q_a + 2 * i * (128 >> 4), b + 2 * i * (kDgBytes >> 4),
+                                                          idesc_s, i != 0);
+          umma_commit(&sm.s_full[n & 1]);
+          if (++s_buf == n_bufs) {
+            s_buf = 0;
+            s_phase ^= 1u;
           }
+        }
+        if (n > 0) {  // O^T += V^T . P^T of tile n - 1, 128 dims at a time, 16 rows an MMA
+          ok = wait_bar(&sm.abort_flag, &sm.p_full[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u, fw);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t a = tile_o + o_buf * (kTileBytes >> 4), b = tile_p + o_buf * (kTileBytes >> 4);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int i = 0; i < kRows / 16; ++i)
+              umma_f16<desc_hi(kDgBytes), desc_hi(kPGroupBytes)>(kOCol + kCols * m,
+                                                                 a + 16 * m * (kDgBytes >> 4) + i * (256 >> 4),
+                                                                 b + i * (256 >> 4), idesc_o, n > 1 || i > 0);
+          umma_commit(&sm.free_[o_buf]);
+          umma_commit(&sm.o_done[(n - 1) & 1]);
+          if (++o_buf == n_bufs) o_buf = 0;
         }
       }
       umma_commit(&sm.done);  // arrives once every MMA issued above has completed
@@ -598,124 +561,98 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     __syncwarp();
   } else if (warp < kFirstSoftmax) {
     // ------------------------------------------------------------ unpack
+    const int set = cw / kUnpackSet;  // takes every other tile
     const int quarter = lane & 3;
     const bool ahead = quarter >= 2, second = (lane & 4) != 0;
-    const int row_u = 8 * cw + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
-    int id = tile_id(u, u.begin);
-    int piece = 0;         // next latent piece of the ring
-    uint32_t phase = 1;    // of its release: the first round finds every piece free
+    const int row_u = 8 * (cw % kUnpackSet) + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
+    int id = tile_id(u, u.begin + set);
     bool ok = true;
-    for (int n = 0; n < n_tiles && ok; ++n) {
-      const int slot = n % n_slots;
+    for (int n = set; n < n_tiles && ok; n += 2) {
+      const int slot = n % n_slots, buf = n % n_bufs;
       // rows that no column sees enter as zeros, whatever the memory holds
-      const int pos = tile_block(u, u.begin + n) * kBlock + row_u;
+      const int pos = tile_pos(u, u.begin + n) + row_u;
       const bool seen = static_cast<unsigned>(id) < pool_blocks && pos < u.stop && (pos < u.sinks || pos >= u.w0);
-      id = tile_id(u, u.begin + n + 1);
-      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[slot], static_cast<uint32_t>(n / n_slots) & 1u, fw);
+      id = tile_id(u, u.begin + n + 2);
+      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[n % (2 * n_slots)], static_cast<uint32_t>(n / (2 * n_slots)) & 1u,
+                         fw);
       if (!ok) break;
-      const uint8_t* row = s_raw + slot * kBlockBytes + row_u * kRowBytes;
+      const uint8_t* row = s_raw + slot * kRawBytes + row_u * kRowBytes;
+      uint8_t* dst = s_tile + buf * kTileBytes + row_u * 16;
       RawPiece<FMT> raw;
-      {
-        uint32_t h[2][4];
-        unpack_rope(*reinterpret_cast<const uint4*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 16 * quarter), h);
-        raw.load(row, 0, quarter, second);
-        if (n >= 2)
-          ok = wait_bar_warp(&sm.abort_flag, &sm.rope_free[n & 1], static_cast<uint32_t>((n >> 1) - 1) & 1u, fw);
-        if (!ok) break;
+      raw.load(row, 0, quarter, second);
+      const uint4 rope = *reinterpret_cast<const uint4*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 16 * quarter);
+      if (n >= n_bufs)
+        ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], static_cast<uint32_t>(n / n_bufs - 1) & 1u, fw);
+      if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(s_rope + (n & 1) * kRopePiece + (2 * quarter + i) * kDgBytes + row_u * 16) =
-              seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
-      }
-      // A piece is published only after the next one's conversion: its stores
-      // have then long landed, which the proxy fence would wait for.
-      uint64_t* stored = &sm.rope_full[n & 1];
-#pragma unroll 1
       for (int m = 0; m < 4; ++m) {
         uint32_t h[4][4];
         raw.unpack(ahead, second, h);
-        warp_publish(stored, lane);
-        if (m < 3) {
-          raw.load(row, m + 1, quarter, second);
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.raw_free[slot]);  // every lane has read its last bytes of the block
-        }
-        ok = wait_bar_warp(&sm.abort_flag, &sm.free_[piece], phase, fw);
-        if (!ok) break;
-        uint8_t* dst = s_lat + piece * kLatPiece + 4 * quarter * kDgBytes + row_u * 16;
+        if (m < 3) raw.load(row, m + 1, quarter, second);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(dst + ((i + (ahead ? 1 : 0)) & 3) * kDgBytes) =
+          *reinterpret_cast<uint4*>(dst + (16 * m + 4 * quarter + ((i + (ahead ? 1 : 0)) & 3)) * kDgBytes) =
               seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
-        stored = &sm.full[piece];
-        if (++piece == n_pieces) {
-          piece = 0;
-          phase ^= 1u;
-        }
       }
-      if (ok) warp_publish(stored, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_free[slot]);  // every lane has read its last bytes of the copy
+      uint32_t h[2][4];
+      unpack_rope(rope, h);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4*>(dst + (kLatent / 8 + 2 * quarter + i) * kDgBytes) =
+            seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
+      warp_publish(&sm.full[buf], lane);
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int sw = warp - kFirstSoftmax;
-    const int quad = warp & 3;        // tensor-memory lanes 32 quad .. 32 quad + 31
-    const int half = sw >> 2;         // columns 32 half .. 32 half + 31
-    const int c_lane = 2 * (lane & 3);
-    const bool has_cols = 32 * half < u.ncols;
+    const int quad = warp & 3;          // tensor-memory lanes 32 quad ..: columns 16 quad .. 16 quad + 15
+    const int t_lane = 2 * (lane & 3);  // rows 8 k + t_lane + e of the tile
+    const int col0 = 16 * quad + (lane >> 2);  // this thread's columns: col0, col0 + 8
+    const bool has_cols = 16 * quad < u.ncols;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-    const int row0 = 16 * quad + (lane >> 2);  // this thread's rows: row0, row0 + 8
-    float qs[8], mr[8];  // scale and maximum of columns 8 k + c_lane + e
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      qs[k] = sm.qscale[32 * half + 8 * (k >> 1) + c_lane + (k & 1)];
-      mr[k] = -INFINITY;
+    const int me = u.me0 + (u.tok_col0 + 16 * quad) / args.num_heads;  // 16 columns share a query token
+    float qs[2] = {0.f, 0.f}, mr[2] = {-INFINITY, -INFINITY};  // scale and (lazy) maximum, base 2
+    float l_part[2] = {0.f, 0.f};  // these rows' share of the denominators
+    if (has_cols) {
+      qs[0] = sm.qscale[col0];
+      qs[1] = sm.qscale[col0 + 8];
     }
-    // 16 columns share a query token
-    const int me[2] = {u.me0 + (u.tok_col0 + 32 * half) / args.num_heads,
-                       u.me0 + (u.tok_col0 + 32 * half + 16) / args.num_heads};
-    float l_part[8];  // these rows' share of the denominators of columns 8 k + c_lane + e
-#pragma unroll
-    for (int j = 0; j < 8; ++j) l_part[j] = 0.f;
     int id = tile_id(u, u.begin);
+    int buf = 0;
     bool aborted = false;
     for (int n = 0; n < n_tiles; ++n) {
+      uint8_t* const tile = s_tile + buf * kTileBytes;
+      if (++buf == n_bufs) buf = 0;
       const bool held = static_cast<unsigned>(id) < pool_blocks;
       id = tile_id(u, u.begin + n + 1);
-      const int pos0 = tile_block(u, u.begin + n) * kBlock + row0;
-      bool vis[2][2];  // [row][16-column half]
+      const int pos0 = tile_pos(u, u.begin + n) + t_lane;
+      uint32_t vis = 0;  // bit 2 k + e: row 8 k + t_lane + e is seen
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int pos = pos0 + 8 * r;
-          vis[r][c] = held && pos < u.stop &&
-                      (!u.masked || (pos <= me[c] && (pos < args.sinks || pos > me[c] - args.window)));
-        }
-      bool ok = wait_bar_warp(&sm.abort_flag, &sm.s_full, static_cast<uint32_t>(n) & 1u, fw);
+      for (int k = 0; k < 8; ++k) {
+        const int pos = pos0 + 8 * (k >> 1) + (k & 1);
+        if (held && pos < u.stop && (!u.masked || (pos <= me && (pos < args.sinks || pos > me - args.window))))
+          vis |= 1u << k;
+      }
+      bool ok = wait_bar_warp(&sm.abort_flag, &sm.s_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, fw);
       tcgen05_fence_after();
-      float z[16];
-      bool nan_row[2] = {false, false}, need = false;
+      float z[16];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
+      uint32_t nan = 0;
+      bool need = false;
       if (has_cols && ok) {
         uint32_t sr[16];
-        tmem_ld_rows16(tbase + lane_base + kCols * (n & 1) + 32 * half, sr);
+        tmem_ld_rows16(lane_base + kRows * (n & 1), sr);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) nan_row[r] = isnan(__uint_as_float(sr[2 * r]));
-        need = nan_row[0] || nan_row[1];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool on = 32 * half + 16 * (k >> 1) < u.ncols;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const bool v = on && vis[r][k >> 1];
-            z[4 * k + 2 * r] = v ? __uint_as_float(sr[4 * k + 2 * r]) * qs[2 * k] : -INFINITY;
-            z[4 * k + 2 * r + 1] = v ? __uint_as_float(sr[4 * k + 2 * r + 1]) * qs[2 * k + 1] : -INFINITY;
-            need |= z[4 * k + 2 * r] > mr[2 * k] + kLazyRaise || z[4 * k + 2 * r + 1] > mr[2 * k + 1] + kLazyRaise;
-          }
+        for (int k = 0; k < 8; ++k) {
+          const float s0 = __uint_as_float(sr[4 * (k >> 1) + (k & 1)]), s1 = __uint_as_float(sr[4 * (k >> 1) + 2 + (k & 1)]);
+          const bool v = (vis >> k & 1u) != 0;
+          if (isnan(s0)) nan |= 1u << k;
+          const float z0 = v ? s0 * qs[0] : -INFINITY, z1 = v ? s1 * qs[1] : -INFINITY;
+          need |= z0 > mr[0] + kLazyRaise || z1 > mr[1] + kLazyRaise;
+          z[4 * (k >> 1) + (k & 1)] = z0;
+          z[4 * (k >> 1) + 2 + (k & 1)] = z1;
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = -INFINITY;
+        need |= nan != 0;
       }
       if (!ok) atomicMin(&sm.abort_tile, n);
       // every softmax thread takes the same branch at every barrier: a failed
@@ -726,135 +663,114 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         break;
       }
       if (raise) {
-        // A cached row that holds a NaN makes its whole row of S NaN.  Columns
-        // that see it get NaN through P; for those that do not, 0 x NaN must
-        // not reach O^T, so the row's values leave the tile.
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (nan_row[r] && half == 0) {
+        // A cached row that holds a NaN makes its whole column of S NaN.  Who
+        // sees it gets NaN through P; for those that do not, 0 x NaN must not
+        // reach O^T, so the row's values leave the tile.
+        if (quad == 0 && nan != 0) {
 #pragma unroll 1
-            for (int dg = lane & 3; dg < kLatent / 8; dg += 4)
-              *reinterpret_cast<uint4*>(s_lat + (4 * n + dg / 16) % n_pieces * kLatPiece + dg % 16 * kDgBytes +
-                                        (row0 + 8 * r) * 16) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) {
+            if ((nan >> k & 1u) == 0) continue;
+            const int row = 8 * (k >> 1) + t_lane + (k & 1);
+            for (int dg = lane >> 2; dg < kLatent / 8; dg += 8)
+              *reinterpret_cast<uint4*>(tile + dg * kDgBytes + row * 16) = make_uint4(0, 0, 0, 0);
           }
-        // maximum of each column: over this thread's two rows, the 8 lanes of
-        // the column's pair, then the four warps of the half
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(z[4 * k + e], z[4 * k + 2 + e]);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-            if (lane < 4) sm.red[4 * half + quad][8 * k + c_lane + e] = m;
-          }
-        named_bar_sync(3, kSoftmaxThreads);
-        if (quad == 0) {
-          const int c = 32 * half + lane;
-          const float m4 = fmaxf(fmaxf(sm.red[4 * half][lane], sm.red[4 * half + 1][lane]),
-                                 fmaxf(sm.red[4 * half + 2][lane], sm.red[4 * half + 3][lane]));
-          const float old = sm.m_ref[c];
-          float al = 1.f;
-          if (m4 > old + kLazyRaise) {
-            al = ex2(old - m4);  // 0 while the maximum is -inf
-            sm.m_ref[c] = m4;
-          }
-          sm.alpha[c] = al;
         }
-        named_bar_sync(3, kSoftmaxThreads);
         bool rescale = false;
+        if (has_cols) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 al = *reinterpret_cast<const float2*>(sm.alpha + 32 * half + 8 * k + c_lane);
-          l_part[2 * k] *= al.x;
-          l_part[2 * k + 1] *= al.y;
-          rescale |= al.x != 1.f || al.y != 1.f;
-          const float2 m = *reinterpret_cast<const float2*>(sm.m_ref + 32 * half + 8 * k + c_lane);
-          mr[2 * k] = m.x;
-          mr[2 * k + 1] = m.y;
-        }
-        // O^T of the previous tiles is complete: S of this one came after it
-        if (n > 0 && has_cols && __any_sync(0xFFFFFFFFu, rescale)) {
-#pragma unroll 1
-          for (int m = 0; m < 8; ++m) {
-            const uint32_t ta = tbase + lane_base + kOCol + kCols * (m >> 1) + 32 * half + 16 * (m & 1);
-            uint32_t o[16];
-            tmem_ld16(ta, o);
+          for (int c = 0; c < 2; ++c) {
+            float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * sm.alpha[32 * half + 16 * (m & 1) + j]);
-            tmem_st16(ta, o);
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(z[4 * k + 2 * c], z[4 * k + 2 * c + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            float al = 1.f;
+            if (m > mr[c] + kLazyRaise) {
+              al = ex2(mr[c] - m);  // 0 while the maximum is -inf
+              mr[c] = m;
+            }
+            l_part[c] *= al;
+            rescale |= al != 1.f;
+            if ((lane & 3) == 0) sm.alpha[col0 + 8 * c] = al;
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        // O^T's columns lie across all four quadrants: each warp scales its lanes
+        if (softmax_any(rescale) && n > 0) {
+          ok = wait_bar_warp(&sm.abort_flag, &sm.o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u, fw);
+          if (!ok) atomicMin(&sm.abort_tile, n + 1);
+          tcgen05_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int m = 0; m < 4 * (u.ncols / 16); ++m) {
+              const int cg = m >> 2;
+              const uint32_t ta = lane_base + kOCol + kCols * (m & 3) + 16 * cg;
+              uint32_t o[16];
+              tmem_ld16(ta, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sm.alpha[16 * cg + j]);
+              tmem_st16(ta, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+          named_bar_sync(3, kSoftmaxThreads);  // alpha may be written again
         }
       }
       if (has_cols) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool on = 32 * half + 16 * (k >> 1) < u.ncols;
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int c = 0; c < 2; ++c) {
             // The denominator sums P before its rounding to f16 (operand type of
             // the product): the LSE keeps float accuracy, and the output's
             // share of that rounding is at most 2^-11.
-            const bool v = on && vis[r][k >> 1];
-            const float p0 = v ? ex2(z[4 * k + 2 * r] - mr[2 * k]) : 0.f;
-            const float p1 = v ? ex2(z[4 * k + 2 * r + 1] - mr[2 * k + 1]) : 0.f;
-            l_part[2 * k] += p0;
-            l_part[2 * k + 1] += p1;
-            const __half2 ph = __floats2half2_rn(p0, p1);
-            *reinterpret_cast<__half2*>(s_rope + (n & 1) * kRopePiece + (4 * half + k) * kDgBytes +
-                                        (row0 + 8 * r) * 16 + 2 * c_lane) = ph;
+            const float p0 = (vis >> (2 * k) & 1u) ? ex2(z[4 * k + 2 * c] - mr[c]) : 0.f;
+            const float p1 = (vis >> (2 * k + 1) & 1u) ? ex2(z[4 * k + 2 * c + 1] - mr[c]) : 0.f;
+            l_part[c] += p0 + p1;
+            *reinterpret_cast<__half2*>(tile + kPOff + (2 * quad + c) * kPGroupBytes + k * 128 + (lane >> 2) * 16 +
+                                        2 * t_lane) = __floats2half2_rn(p0, p1);
           }
-        }
       }
       tcgen05_fence_before();
-      warp_publish(&sm.p_full, lane);
+      if (ok) warp_publish(&sm.p_full[n & 1], lane);
     }
     // ---- denominators and LSEs, once every product is done
     const bool ok = !aborted && wait_bar_warp(&sm.abort_flag, &sm.done, 0u, fw);
     if (!ok) atomicMin(&sm.abort_tile, -1);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = l_part[2 * k + e];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-        if (lane < 4) sm.red[4 * half + quad][8 * k + c_lane + e] = l;
-      }
-    named_bar_sync(3, kSoftmaxThreads);
-    if (quad == 0 && 32 * half + lane < u.ncols) {
-      const int c = 32 * half + lane;
-      const float lt = (sm.red[4 * half][lane] + sm.red[4 * half + 1][lane]) +
-                       (sm.red[4 * half + 2][lane] + sm.red[4 * half + 3][lane]);
-      sm.alpha[c] = lt == 0.f ? 0.f : 1.f / lt;  // 0 when the column saw nothing
-      const float lse2 = lt == 0.f ? -INFINITY : sm.m_ref[c] + lg2(lt);
-      if (*reinterpret_cast<volatile int*>(&sm.abort_tile) >= 0) {
-        if (!direct)
-          args.part_lse[(u.col0 + c) * args.parts + u.part] = lse2;
-        else if (args.lse != nullptr)
-          args.lse[u.col0 + c] = lse2 * kLn2f;
+    for (int c = 0; c < 2; ++c) {
+      float l = l_part[c];
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+      if ((lane & 3) == 0 && has_cols) {
+        const int col = col0 + 8 * c;
+        sm.alpha[col] = l == 0.f ? 0.f : 1.f / l;  // 0 when the column saw nothing
+        const float lse2 = l == 0.f ? -INFINITY : mr[c] + lg2(l);
+        if (ok && !direct)
+          args.part_lse[(u.col0 + col) * args.parts + u.part] = lse2;
+        else if (ok && args.lse != nullptr)
+          args.lse[u.col0 + col] = lse2 * kLn2f;
       }
     }
   }
 
-  // ---- output: a warp has its quadrant's tensor-memory lanes and 16 columns
+  // ---- output: a warp has its quadrant's tensor-memory lanes; the three warps
+  // of a quadrant share the pieces of 128 dims x 16 columns
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp >= kFirstUnpack && 16 * (cw >> 2) < u.ncols && *reinterpret_cast<volatile int*>(&sm.abort_tile) >= 0) {
-    const int quad = warp & 3, cq = cw >> 2;
+  if (warp >= kFirstUnpack && *reinterpret_cast<volatile int*>(&sm.abort_tile) == kNoAbort) {
+    const int quad = warp & 3;
 #pragma unroll 1
-    for (int m = 0; m < 4; ++m) {
+    for (int piece = cw >> 2; piece < 4 * (u.ncols / 16); piece += kWarps / 4) {
+      const int m = piece & 3, cg = piece >> 2;
       uint32_t o[16];
-      tmem_ld16(tbase + (static_cast<uint32_t>(32 * quad) << 16) + kOCol + kCols * m + 16 * cq, o);
+      tmem_ld16((static_cast<uint32_t>(32 * quad) << 16) + kOCol + kCols * m + 16 * cg, o);
       const int dim = 128 * m + 32 * quad + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float inv = sm.alpha[16 * cq + j];
+        const float inv = sm.alpha[16 * cg + j];
         const float x = inv == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
-        const int64_t col = u.col0 + 16 * cq + j;
+        const int64_t col = u.col0 + 16 * cg + j;
         if (direct)
           args.out[col * kLatent + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
         else  // a convex combination of cached values (|x| <= 6 x 448): f16 keeps 11 significant bits
@@ -867,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   // its tensor memory
   if (warp == kCopyWarp && lane == 0) {
     for (int n = max(0, copied - n_slots); n < copied; ++n)
-      mbar_wait_bounded(&sm.raw_full[n % n_slots], static_cast<uint32_t>(n / n_slots) & 1u, fw, kFaultDecodeWait);
+      mbar_wait_bounded(&sm.raw_full[n % (2 * n_slots)], static_cast<uint32_t>(n / (2 * n_slots)) & 1u, fw,
+                        kFaultDecodeWait);
   }
   if (warp == kMmaWarp && lane == 0) mbar_wait_bounded(&sm.done, 0u, fw, kFaultDecodeWait);
   tcgen05_fence_before();
@@ -952,10 +869,10 @@ cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, 
 // (start-up, query load and output, in tiles), of the call = full waves of
 // the prefix's CTAs, with the own rows' CTAs (no longer than the prefix's) in
 // the SMs that the last of those waves leaves idle and in waves of their own
-// after it, + the joining of the partials (about two tiles, and one for every
-// 12).  In eighths of a tile; the fewest partials among equals.
+// after it, + the joining of the partials (about four tiles, and one for every
+// 6).  In eighths of a tile; the fewest partials among equals.
 DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_rows, int prefix_len) {
-  constexpr int64_t kStartTiles = 4;
+  constexpr int64_t kStartTiles = 8;
   DensePlan p{1, 1, 0, 0, 0};
   const int64_t sms = device_sm_count();
   const int64_t req_cols = static_cast<int64_t>(q_len) * num_heads;
@@ -979,7 +896,7 @@ DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_row
       const int64_t fit = (waves * sms - groups * n) * ((slice + kStartTiles) / (own_slice + kStartTiles));
       if (own_groups * s > fit) cost += 8 * ((own_groups * s - fit + sms - 1) / sms) * (own_slice + kStartTiles);
     }
-    if (n + s > 1) cost += 16 + 2 * (n + s) / 3;
+    if (n + s > 1) cost += 32 + 4 * (n + s) / 3;
     if (best < 0 || cost < best) {
       best = cost;
       p.prefix_splits = static_cast<int>(pre_tiles > 0 ? n : 0);
