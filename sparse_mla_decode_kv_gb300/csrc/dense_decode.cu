@@ -48,18 +48,18 @@ constexpr int kRows = 32;  // rows per tile: half a cache block
 constexpr int kCols = 64;  // columns per CTA
 // Warp 0 issues the MMAs (a warp's instructions wait for those of older warps
 // on its scheduler: as the youngest, it issued one MMA in ~200 cycles), warp 1
-// copies, then the unpack and the softmax warps.
+// copies, then the softmax and, as the youngest, the unpack warps.
 constexpr int kMmaWarp = 0;
 constexpr int kCopyWarp = 1;
-constexpr int kFirstUnpack = 2;
+constexpr int kFirstSoftmax = 2;
+constexpr int kSoftmaxWarps = 4;  // one per tensor-memory quadrant
+constexpr int kFirstUnpack = kFirstSoftmax + kSoftmaxWarps;
 constexpr int kUnpackSet = 4;  // warps that unpack one tile, 8 rows each
 constexpr int kUnpackWarps = 2 * kUnpackSet;
-constexpr int kFirstSoftmax = kFirstUnpack + kUnpackWarps;
-constexpr int kSoftmaxWarps = 4;  // one per tensor-memory quadrant
 constexpr int kWarps = kUnpackWarps + kSoftmaxWarps;
 constexpr int kComputeThreads = kWarps * 32;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kThreads = kComputeThreads + 32 * kFirstUnpack;
+constexpr int kThreads = kComputeThreads + 32 * kFirstSoftmax;
 constexpr int kDimGroups = (kLatent + kRope) / 8;  // 72
 // One 8-dim group of a tile: 16 bytes a row and 16 bytes of padding, see
 // RawPiece.
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   constexpr uint32_t kRawBytes = kRows * kRowBytes;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int cw = warp - kFirstUnpack, ct = threadIdx.x - 32 * kFirstUnpack;  // among the unpack and softmax warps
+  const int cw = warp - kFirstSoftmax, ct = threadIdx.x - 32 * kFirstSoftmax;  // among the softmax and unpack warps
   unsigned int* fw = args.fault_word;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     }
     return;
   }
-  if (warp >= kFirstUnpack && ct < kCols) sm.qmax[ct] = 0;
+  if (warp >= kFirstSoftmax && ct < kCols) sm.qmax[ct] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sm.raw_full[i], 1);
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   if (warp == kCopyWarp && lane == 0) {  // the first tiles arrive while the query is converted
     for (int n = 0; n < n_slots && n < n_tiles; ++n) copy_tile(n, tile_id(u, u.begin + n));
   }
-  if (warp >= kFirstUnpack) {
+  if (warp >= kFirstSoftmax) {
     // The query, bf16 -> f16 core matrices of 8 columns x 8 dims.  A warp moves
     // 8 columns x 32 dims at a time (64-byte pieces of 8 rows in, conflict-free
     // 16-byte stores out); every load is issued before the first is used.  A
@@ -559,22 +559,23 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       umma_commit(&sm.done);  // arrives once every MMA issued above has completed
     }
     __syncwarp();
-  } else if (warp < kFirstSoftmax) {
+  } else if (warp >= kFirstUnpack) {
     // ------------------------------------------------------------ unpack
-    const int set = cw / kUnpackSet;  // takes every other tile
+    const int uw = warp - kFirstUnpack;
+    const int set = uw / kUnpackSet;  // takes every other tile
     const int quarter = lane & 3;
     const bool ahead = quarter >= 2, second = (lane & 4) != 0;
-    const int row_u = 8 * (cw % kUnpackSet) + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
+    const int row_u = 8 * (uw % kUnpackSet) + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
     int id = tile_id(u, u.begin + set);
     bool ok = true;
+    int slot = set, full = set, buf = set;  // tile n's copy, its barrier, its unpacked place
+    uint32_t full_phase = 0, free_phase = 1;
     for (int n = set; n < n_tiles && ok; n += 2) {
-      const int slot = n % n_slots, buf = n % n_bufs;
       // rows that no column sees enter as zeros, whatever the memory holds
       const int pos = tile_pos(u, u.begin + n) + row_u;
       const bool seen = static_cast<unsigned>(id) < pool_blocks && pos < u.stop && (pos < u.sinks || pos >= u.w0);
       id = tile_id(u, u.begin + n + 2);
-      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[n % (2 * n_slots)], static_cast<uint32_t>(n / (2 * n_slots)) & 1u,
-                         fw);
+      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[full], full_phase, fw);
       if (!ok) break;
       const uint8_t* row = s_raw + slot * kRawBytes + row_u * kRowBytes;
       uint8_t* dst = s_tile + buf * kTileBytes + row_u * 16;
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       raw.load(row, 0, quarter, second);
       const uint4 rope = *reinterpret_cast<const uint4*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 16 * quarter);
       if (n >= n_bufs)
-        ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], static_cast<uint32_t>(n / n_bufs - 1) & 1u, fw);
+        ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], free_phase, fw);
       if (!ok) break;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -603,6 +604,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         *reinterpret_cast<uint4*>(dst + (kLatent / 8 + 2 * quarter + i) * kDgBytes) =
             seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
       warp_publish(&sm.full[buf], lane);
+      if ((slot += 2) >= n_slots) slot -= n_slots;
+      if ((full += 2) >= 2 * n_slots) {
+        full -= 2 * n_slots;
+        full_phase ^= 1u;
+      }
+      if ((buf += 2) >= n_bufs) {
+        buf -= n_bufs;
+        free_phase ^= 1u;
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -618,22 +628,26 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       qs[0] = sm.qscale[col0];
       qs[1] = sm.qscale[col0 + 8];
     }
-    int id = tile_id(u, u.begin);
+    // bit 2 k + e: row 8 k + t_lane + e of tile n, in block `id`, is seen
+    auto seen_rows = [&](int n, int id) -> uint32_t {
+      if (static_cast<unsigned>(id) >= pool_blocks) return 0;
+      const int first = tile_pos(u, u.begin + n), last = first + kRows - 1;
+      if (last < u.stop && (!u.masked || (last <= me && (last < args.sinks || first > me - args.window)))) return 0xFFu;
+      uint32_t v = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int pos = first + t_lane + 8 * (k >> 1) + (k & 1);
+        if (pos < u.stop && (!u.masked || (pos <= me && (pos < args.sinks || pos > me - args.window)))) v |= 1u << k;
+      }
+      return v;
+    };
+    uint32_t vis = seen_rows(0, tile_id(u, u.begin));
+    int id = tile_id(u, u.begin + 1);
     int buf = 0;
     bool aborted = false;
     for (int n = 0; n < n_tiles; ++n) {
       uint8_t* const tile = s_tile + buf * kTileBytes;
       if (++buf == n_bufs) buf = 0;
-      const bool held = static_cast<unsigned>(id) < pool_blocks;
-      id = tile_id(u, u.begin + n + 1);
-      const int pos0 = tile_pos(u, u.begin + n) + t_lane;
-      uint32_t vis = 0;  // bit 2 k + e: row 8 k + t_lane + e is seen
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int pos = pos0 + 8 * (k >> 1) + (k & 1);
-        if (held && pos < u.stop && (!u.masked || (pos <= me && (pos < args.sinks || pos > me - args.window))))
-          vis |= 1u << k;
-      }
       bool ok = wait_bar_warp(&sm.abort_flag, &sm.s_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, fw);
       tcgen05_fence_after();
       float z[16];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
@@ -732,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       }
       tcgen05_fence_before();
       if (ok) warp_publish(&sm.p_full[n & 1], lane);
+      vis = seen_rows(n + 1, id);
+      id = tile_id(u, u.begin + n + 2);
     }
     // ---- denominators and LSEs, once every product is done
     const bool ok = !aborted && wait_bar_warp(&sm.abort_flag, &sm.done, 0u, fw);
@@ -758,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp >= kFirstUnpack && *reinterpret_cast<volatile int*>(&sm.abort_tile) == kNoAbort) {
+  if (warp >= kFirstSoftmax && *reinterpret_cast<volatile int*>(&sm.abort_tile) == kNoAbort) {
     const int quad = warp & 3;
 #pragma unroll 1
     for (int piece = cw >> 2; piece < 4 * (u.ncols / 16); piece += kWarps / 4) {
