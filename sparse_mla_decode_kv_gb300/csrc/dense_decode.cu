@@ -52,10 +52,9 @@ constexpr int kCols = 64;  // columns per CTA
 constexpr int kMmaWarp = 0;
 constexpr int kCopyWarp = 1;
 constexpr int kFirstSoftmax = 2;
-constexpr int kSoftmaxWarps = 4;  // one per tensor-memory quadrant
+constexpr int kSoftmaxWarps = 8;  // two per tensor-memory quadrant: 16 columns x 16 rows of a tile each
 constexpr int kFirstUnpack = kFirstSoftmax + kSoftmaxWarps;
-constexpr int kUnpackSet = 4;  // warps that unpack one tile, 8 rows each
-constexpr int kUnpackWarps = 2 * kUnpackSet;
+constexpr int kUnpackWarps = 8;  // 8 rows x half the dims each
 constexpr int kWarps = kUnpackWarps + kSoftmaxWarps;
 constexpr int kComputeThreads = kWarps * 32;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
@@ -79,12 +78,11 @@ constexpr float kLazyRaise = 8.f;
 constexpr float kLn2f = 0.6931471805599453f;
 
 struct Ctl {              // the fixed part of shared memory, at its start
+  float part[2][kCols];   // the row halves' maxima (at a raise) and denominators (at the end)
   float alpha[kCols];     // factor of the last raise; at the end 1 / denominator
   float qscale[kCols];    // softmax scale (base 2) x 2^-shift of the column's query
   uint32_t qmax[kCols];   // largest |q| of the column (bf16 magnitude bits)
-  // raw_full: tile n's is the (n % (2 slots))-th, so that each has waiters of one
-  // unpack set only, which see all its phases even where the slots are three.
-  uint64_t raw_full[2 * kMaxSlots], raw_free[kMaxSlots], full[kMaxTiles], free_[kMaxTiles];
+  uint64_t raw_full[kMaxSlots], raw_free[kMaxSlots], full[kMaxTiles], free_[kMaxTiles];
   uint64_t s_full[2], p_full[2], o_done[2], done;
   uint32_t tmem_base;
   int abort_flag;  // set by whoever ran out of polls; ends the others' waits
@@ -155,15 +153,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 16 lanes x 32 columns of this warp's quadrant (rows 16 quad .. 16 quad + 15
+// 16 lanes x 16 columns of this warp's quadrant (rows 16 quad .. 16 quad + 15
 // of an M = 64 accumulator) in the matrix-fragment layout: r[4 k + e] is row
 // lane / 4 + 8 (e / 2), column 8 k + 2 (lane % 4) + e % 2.
-__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_rows8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // OR of `pred` over the softmax warps (named barrier 2).
@@ -215,9 +211,13 @@ template <>
 struct RawPiece<0> {
   uint4 c;
   uint32_t two;  // the two scales
-  __device__ __forceinline__ void load(const uint8_t* row, int m, int quarter, bool) {
+  __device__ __forceinline__ void load(const uint8_t* row, int m, int quarter, bool, bool seen) {
     c = *reinterpret_cast<const uint4*>(row + 64 * m + 16 * quarter);
     two = *reinterpret_cast<const unsigned short*>(row + kScaleOff + 8 * m + 2 * quarter);
+    if (!seen) {
+      c = make_uint4(0, 0, 0, 0);
+      two = 0;
+    }
   }
   __device__ __forceinline__ void unpack(bool ahead, bool, uint32_t (&h)[4][4]) const {
     const uint32_t s0 = e4m3x2_to_f16x2((two & 0xFFu) * 0x0101u), s1 = e4m3x2_to_f16x2((two >> 8) * 0x0101u);
@@ -234,10 +234,11 @@ struct RawPiece<0> {
 template <>
 struct RawPiece<1> {
   uint4 x, y;
-  __device__ __forceinline__ void load(const uint8_t* row, int m, int quarter, bool second) {
+  __device__ __forceinline__ void load(const uint8_t* row, int m, int quarter, bool second, bool seen) {
     const uint8_t* p = row + 128 * m + 32 * quarter;
     x = *reinterpret_cast<const uint4*>(p + (second ? 16 : 0));
     y = *reinterpret_cast<const uint4*>(p + (second ? 0 : 16));
+    if (!seen) x = y = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void unpack(bool ahead, bool second, uint32_t (&h)[4][4]) const {
     const uint4 c0 = second ? y : x, c1 = second ? x : y;
@@ -254,20 +255,6 @@ struct RawPiece<1> {
     }
   }
 };
-__device__ __forceinline__ void unpack_rope(const uint4 v, uint32_t (&h)[2][4]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t lo[2], hi[2];
-    e4m3x4_to_f16x2x2(w[2 * i], lo);
-    e4m3x4_to_f16x2x2(w[2 * i + 1], hi);
-    h[i][0] = lo[0];
-    h[i][1] = lo[1];
-    h[i][2] = hi[0];
-    h[i][3] = hi[1];
-  }
-}
-
 // One CTA's work: columns [col0, col0 + ncols) over tiles [begin, end) of a
 // list.  Tile t is the t-th 32 positions for t < n_sink_tiles, else the (w_tile
 // + t - n_sink_tiles)-th.  Positions in [0, stop) that lie in the first
@@ -386,11 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_full[kMaxSlots + i], 1);
-      mbar_init(&sm.raw_free[i], kUnpackSet);
+      mbar_init(&sm.raw_free[i], kUnpackWarps);
     }
     for (int i = 0; i < kMaxTiles; ++i) {
-      mbar_init(&sm.full[i], kUnpackSet);
+      mbar_init(&sm.full[i], kUnpackWarps);
       mbar_init(&sm.free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -422,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     const int slot = n % n_slots;
     if (n >= n_slots && !wait_bar(&sm.abort_flag, &sm.raw_free[slot], static_cast<uint32_t>(n / n_slots - 1) & 1u, fw))
       return false;
-    uint64_t* const full = &sm.raw_full[n % (2 * n_slots)];
+    uint64_t* const full = &sm.raw_full[slot];
     if (static_cast<unsigned>(id) < pool_blocks) {
       mbar_expect_tx(full, kRawBytes);
       bulk_load(s_raw + slot * kRawBytes,
@@ -445,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     // column whose query holds an infinity or NaN enters as zeros with a NaN
     // scale: its results are NaN, its neighbours' are not.
     constexpr int kPieces = kDimGroups / 4;               // of 32 dims
-    constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 12
+    constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 9
     const int n_tasks = (u.ncols / 8) * kPieces;
     uint4 x[kPer];
 #pragma unroll
@@ -562,62 +548,62 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   } else if (warp >= kFirstUnpack) {
     // ------------------------------------------------------------ unpack
     const int uw = warp - kFirstUnpack;
-    const int set = uw / kUnpackSet;  // takes every other tile
+    const int half = uw >> 2;  // dims 256 half .. 256 half + 255 and rope dims 32 half .. 32 half + 31
     const int quarter = lane & 3;
     const bool ahead = quarter >= 2, second = (lane & 4) != 0;
-    const int row_u = 8 * (uw % kUnpackSet) + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
-    int id = tile_id(u, u.begin + set);
+    const int row_u = 8 * (uw & 3) + ((lane >> 3) & 1) + (lane >> 4) * 4 + (second ? 2 : 0);
+    int id = tile_id(u, u.begin);
     bool ok = true;
-    int slot = set, full = set, buf = set;  // tile n's copy, its barrier, its unpacked place
+    int slot = 0, buf = 0;
     uint32_t full_phase = 0, free_phase = 1;
-    for (int n = set; n < n_tiles && ok; n += 2) {
+    for (int n = 0; n < n_tiles && ok; ++n) {
       // rows that no column sees enter as zeros, whatever the memory holds
       const int pos = tile_pos(u, u.begin + n) + row_u;
       const bool seen = static_cast<unsigned>(id) < pool_blocks && pos < u.stop && (pos < u.sinks || pos >= u.w0);
-      id = tile_id(u, u.begin + n + 2);
-      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[full], full_phase, fw);
+      id = tile_id(u, u.begin + n + 1);
+      ok = wait_bar_warp(&sm.abort_flag, &sm.raw_full[slot], full_phase, fw);
       if (!ok) break;
       const uint8_t* row = s_raw + slot * kRawBytes + row_u * kRowBytes;
       uint8_t* dst = s_tile + buf * kTileBytes + row_u * 16;
-      RawPiece<FMT> raw;
-      raw.load(row, 0, quarter, second);
-      const uint4 rope = *reinterpret_cast<const uint4*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 16 * quarter);
-      if (n >= n_bufs)
-        ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], free_phase, fw);
+      RawPiece<FMT> raw[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) raw[m].load(row, 2 * half + m, quarter, second, seen);
+      uint2 rope = *reinterpret_cast<const uint2*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 32 * half +
+                                                   8 * quarter);
+      if (!seen) rope = make_uint2(0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_free[slot]);  // the copy has been read
+      if (n >= n_bufs) ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], free_phase, fw);
       if (!ok) break;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < 2; ++m) {
         uint32_t h[4][4];
-        raw.unpack(ahead, second, h);
-        if (m < 3) raw.load(row, m + 1, quarter, second);
+        raw[m].unpack(ahead, second, h);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(dst + (16 * m + 4 * quarter + ((i + (ahead ? 1 : 0)) & 3)) * kDgBytes) =
-              seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (32 * half + 16 * m + 4 * quarter + ((i + (ahead ? 1 : 0)) & 3)) * kDgBytes) =
+              make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.raw_free[slot]);  // every lane has read its last bytes of the copy
-      uint32_t h[2][4];
-      unpack_rope(rope, h);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint4*>(dst + (kLatent / 8 + 2 * quarter + i) * kDgBytes) =
-            seen ? make_uint4(h[i][0], h[i][1], h[i][2], h[i][3]) : make_uint4(0, 0, 0, 0);
+      uint32_t lo[2], hi[2];
+      e4m3x4_to_f16x2x2(rope.x, lo);
+      e4m3x4_to_f16x2x2(rope.y, hi);
+      *reinterpret_cast<uint4*>(dst + (kLatent / 8 + 4 * half + quarter) * kDgBytes) =
+          make_uint4(lo[0], lo[1], hi[0], hi[1]);
       warp_publish(&sm.full[buf], lane);
-      if ((slot += 2) >= n_slots) slot -= n_slots;
-      if ((full += 2) >= 2 * n_slots) {
-        full -= 2 * n_slots;
+      if (++slot == n_slots) {
+        slot = 0;
         full_phase ^= 1u;
       }
-      if ((buf += 2) >= n_bufs) {
-        buf -= n_bufs;
+      if (++buf == n_bufs) {
+        buf = 0;
         free_phase ^= 1u;
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3;          // tensor-memory lanes 32 quad ..: columns 16 quad .. 16 quad + 15
-    const int t_lane = 2 * (lane & 3);  // rows 8 k + t_lane + e of the tile
+    const int rh = cw >> 2;             // rows 16 rh .. 16 rh + 15 of a tile
+    const int t_lane = 2 * (lane & 3);  // of them, rows 8 k + t_lane + e
     const int col0 = 16 * quad + (lane >> 2);  // this thread's columns: col0, col0 + 8
     const bool has_cols = 16 * quad < u.ncols;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
@@ -628,14 +614,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       qs[0] = sm.qscale[col0];
       qs[1] = sm.qscale[col0 + 8];
     }
-    // bit 2 k + e: row 8 k + t_lane + e of tile n, in block `id`, is seen
+    // bit 2 k + e: row 8 k + t_lane + e of this half of tile n, in block `id`, is seen
     auto seen_rows = [&](int n, int id) -> uint32_t {
       if (static_cast<unsigned>(id) >= pool_blocks) return 0;
-      const int first = tile_pos(u, u.begin + n), last = first + kRows - 1;
-      if (last < u.stop && (!u.masked || (last <= me && (last < args.sinks || first > me - args.window)))) return 0xFFu;
+      const int first = tile_pos(u, u.begin + n) + 16 * rh, last = first + 15;
+      if (last < u.stop && (!u.masked || (last <= me && (last < args.sinks || first > me - args.window)))) return 15u;
       uint32_t v = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         const int pos = first + t_lane + 8 * (k >> 1) + (k & 1);
         if (pos < u.stop && (!u.masked || (pos <= me && (pos < args.sinks || pos > me - args.window)))) v |= 1u << k;
       }
@@ -650,23 +636,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       if (++buf == n_bufs) buf = 0;
       bool ok = wait_bar_warp(&sm.abort_flag, &sm.s_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, fw);
       tcgen05_fence_after();
-      float z[16];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
-      uint32_t nan = 0;
+      float z[8];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
+      float nan_sum = 0.f, top[2] = {-INFINITY, -INFINITY};
       bool need = false;
       if (has_cols && ok) {
-        uint32_t sr[16];
-        tmem_ld_rows16(lane_base + kRows * (n & 1), sr);
+        uint32_t sr[8];
+        tmem_ld_rows8(lane_base + kRows * (n & 1) + 16 * rh, sr);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const float s0 = __uint_as_float(sr[4 * (k >> 1) + (k & 1)]), s1 = __uint_as_float(sr[4 * (k >> 1) + 2 + (k & 1)]);
-          const bool v = (vis >> k & 1u) != 0;
-          if (isnan(s0)) nan |= 1u << k;
-          const float z0 = v ? s0 * qs[0] : -INFINITY, z1 = v ? s1 * qs[1] : -INFINITY;
-          need |= z0 > mr[0] + kLazyRaise || z1 > mr[1] + kLazyRaise;
-          z[4 * (k >> 1) + (k & 1)] = z0;
-          z[4 * (k >> 1) + 2 + (k & 1)] = z1;
+          nan_sum += s0;  // S is bounded: the sum is NaN where a row holds one
+          z[4 * (k >> 1) + (k & 1)] = s0 * qs[0];
+          z[4 * (k >> 1) + 2 + (k & 1)] = s1 * qs[1];
         }
-        need |= nan != 0;
+        if (vis != 15u) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((vis >> k & 1u) == 0) z[4 * (k >> 1) + (k & 1)] = z[4 * (k >> 1) + 2 + (k & 1)] = -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          top[c] = fmaxf(fmaxf(z[2 * c], z[2 * c + 1]), fmaxf(z[4 + 2 * c], z[4 + 2 * c + 1]));
+        need = isnan(nan_sum) || top[0] > mr[0] + kLazyRaise || top[1] > mr[1] + kLazyRaise;
       }
       if (!ok) atomicMin(&sm.abort_tile, n);
       // every softmax thread takes the same branch at every barrier: a failed
@@ -680,24 +671,32 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         // A cached row that holds a NaN makes its whole column of S NaN.  Who
         // sees it gets NaN through P; for those that do not, 0 x NaN must not
         // reach O^T, so the row's values leave the tile.
-        if (quad == 0 && nan != 0) {
+        if (quad == 0 && __any_sync(0xFFFFFFFFu, isnan(nan_sum))) {
+          uint32_t sr[8];
+          tmem_ld_rows8(lane_base + kRows * (n & 1) + 16 * rh, sr);
+          uint32_t rows = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rows |= isnan(__uint_as_float(sr[4 * (k >> 1) + (k & 1)])) ? 1u << k : 0u;
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            if ((nan >> k & 1u) == 0) continue;
-            const int row = 8 * (k >> 1) + t_lane + (k & 1);
+          for (int k = 0; k < 4; ++k) {
+            if ((rows >> k & 1u) == 0) continue;
+            const int row = 16 * rh + 8 * (k >> 1) + t_lane + (k & 1);
             for (int dg = lane >> 2; dg < kLatent / 8; dg += 8)
               *reinterpret_cast<uint4*>(tile + dg * kDgBytes + row * 16) = make_uint4(0, 0, 0, 0);
           }
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 1));
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 2));
+          if ((lane & 3) == 0) sm.part[rh][col0 + 8 * c] = top[c];
+        }
+        named_bar_sync(3, kSoftmaxThreads);
         bool rescale = false;
         if (has_cols) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(z[4 * k + 2 * c], z[4 * k + 2 * c + 1]));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            const float m = fmaxf(top[c], sm.part[rh ^ 1][col0 + 8 * c]);
             float al = 1.f;
             if (m > mr[c] + kLazyRaise) {
               al = ex2(mr[c] - m);  // 0 while the maximum is -inf
@@ -705,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
             }
             l_part[c] *= al;
             rescale |= al != 1.f;
-            if ((lane & 3) == 0) sm.alpha[col0 + 8 * c] = al;
+            if ((lane & 3) == 0 && rh == 0) sm.alpha[col0 + 8 * c] = al;
           }
         }
         // O^T's columns lie across all four quadrants: each warp scales its lanes
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
           tcgen05_fence_after();
           if (ok) {
 #pragma unroll 1
-            for (int m = 0; m < 4 * (u.ncols / 16); ++m) {
+            for (int m = rh; m < 4 * (u.ncols / 16); m += 2) {
               const int cg = m >> 2;
               const uint32_t ta = lane_base + kOCol + kCols * (m & 3) + 16 * cg;
               uint32_t o[16];
@@ -730,18 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         }
       }
       if (has_cols) {
+        // a masked z is -inf, and so is the maximum of a column that has seen nothing
+        const float sub[2] = {mr[0] == -INFINITY ? 0.f : mr[0], mr[1] == -INFINITY ? 0.f : mr[1]};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             // The denominator sums P before its rounding to f16 (operand type of
             // the product): the LSE keeps float accuracy, and the output's
             // share of that rounding is at most 2^-11.
-            const float p0 = (vis >> (2 * k) & 1u) ? ex2(z[4 * k + 2 * c] - mr[c]) : 0.f;
-            const float p1 = (vis >> (2 * k + 1) & 1u) ? ex2(z[4 * k + 2 * c + 1] - mr[c]) : 0.f;
+            const float p0 = ex2(z[4 * k + 2 * c] - sub[c]), p1 = ex2(z[4 * k + 2 * c + 1] - sub[c]);
             l_part[c] += p0 + p1;
-            *reinterpret_cast<__half2*>(tile + kPOff + (2 * quad + c) * kPGroupBytes + k * 128 + (lane >> 2) * 16 +
-                                        2 * t_lane) = __floats2half2_rn(p0, p1);
+            *reinterpret_cast<__half2*>(tile + kPOff + (2 * quad + c) * kPGroupBytes + (2 * rh + k) * 128 +
+                                        (lane >> 2) * 16 + 2 * t_lane) = __floats2half2_rn(p0, p1);
           }
       }
       tcgen05_fence_before();
@@ -754,11 +754,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     if (!ok) atomicMin(&sm.abort_tile, -1);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float l = l_part[c];
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-      if ((lane & 3) == 0 && has_cols) {
+      l_part[c] += __shfl_xor_sync(0xFFFFFFFFu, l_part[c], 1);
+      l_part[c] += __shfl_xor_sync(0xFFFFFFFFu, l_part[c], 2);
+      if ((lane & 3) == 0) sm.part[rh][col0 + 8 * c] = l_part[c];
+    }
+    named_bar_sync(4, kSoftmaxThreads);
+    if ((lane & 3) == 0 && has_cols && rh == 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         const int col = col0 + 8 * c;
+        const float l = l_part[c] + sm.part[1][col];
         sm.alpha[col] = l == 0.f ? 0.f : 1.f / l;  // 0 when the column saw nothing
         const float lse2 = l == 0.f ? -INFINITY : mr[c] + lg2(l);
         if (ok && !direct)
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     }
   }
 
-  // ---- output: a warp has its quadrant's tensor-memory lanes; the three warps
+  // ---- output: a warp has its quadrant's tensor-memory lanes; the four warps
   // of a quadrant share the pieces of 128 dims x 16 columns
   tcgen05_fence_before();
   __syncthreads();
@@ -799,8 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   // its tensor memory
   if (warp == kCopyWarp && lane == 0) {
     for (int n = max(0, copied - n_slots); n < copied; ++n)
-      mbar_wait_bounded(&sm.raw_full[n % (2 * n_slots)], static_cast<uint32_t>(n / (2 * n_slots)) & 1u, fw,
-                        kFaultDecodeWait);
+      mbar_wait_bounded(&sm.raw_full[n % n_slots], static_cast<uint32_t>(n / n_slots) & 1u, fw, kFaultDecodeWait);
   }
   if (warp == kMmaWarp && lane == 0) mbar_wait_bounded(&sm.done, 0u, fw, kFaultDecodeWait);
   tcgen05_fence_before();
