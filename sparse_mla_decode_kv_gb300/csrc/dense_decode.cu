@@ -83,7 +83,7 @@ struct Ctl {              // the fixed part of shared memory, at its start
   float qscale[kCols];    // softmax scale (base 2) x 2^-shift of the column's query
   uint32_t qmax[kCols];   // largest |q| of the column (bf16 magnitude bits)
   uint64_t raw_full[kMaxSlots], raw_free[kMaxSlots], full[kMaxTiles], free_[kMaxTiles];
-  uint64_t s_full[2], p_full[2], o_done[2], done;
+  uint64_t s_full[2], p_full[2], done;
   uint32_t tmem_base;
   int abort_flag;  // set by whoever ran out of polls; ends the others' waits
   int abort_tile;  // first tile whose barrier a softmax warp reached with a failed wait
@@ -185,8 +185,8 @@ __device__ __forceinline__ bool wait_bar(int* abort_flag, uint64_t* bar, uint32_
 // The same for a whole warp: one lane polls.
 __device__ __forceinline__ bool wait_bar_warp(int* abort_flag, uint64_t* bar, uint32_t parity, unsigned int* fw) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(abort_flag, bar, parity, fw);
-  return __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+  if (!mbar_try_wait(bar, parity)) ok = wait_bar(abort_flag, bar, parity, fw);
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 // One arrival per warp after all its lanes' shared-memory writes: each lane
 // publishes its own writes to the tensor core's proxy first.
@@ -382,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], kSoftmaxWarps);
-      mbar_init(&sm.o_done[i], 1);
     }
     mbar_init(&sm.done, 1);
     sm.abort_flag = 0;
@@ -538,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
                                                                  a + 16 * m * (kDgBytes >> 4) + i * (256 >> 4),
                                                                  b + i * (256 >> 4), idesc_o, n > 1 || i > 0);
           umma_commit(&sm.free_[o_buf]);
-          umma_commit(&sm.o_done[(n - 1) & 1]);
           if (++o_buf == n_bufs) o_buf = 0;
         }
       }
@@ -638,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       tcgen05_fence_after();
       float z[8];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
       float nan_sum = 0.f, top[2] = {-INFINITY, -INFINITY};
-      bool need = false;
+      bool need = !ok;
       if (has_cols && ok) {
         uint32_t sr[8];
         tmem_ld_rows8(lane_base + kRows * (n & 1) + 16 * rh, sr);
@@ -662,12 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       if (!ok) atomicMin(&sm.abort_tile, n);
       // every softmax thread takes the same branch at every barrier: a failed
       // wait is recorded with its tile before that tile's barrier
-      const bool raise = softmax_any(need);
-      if (*reinterpret_cast<volatile int*>(&sm.abort_tile) <= n) {
-        aborted = true;
-        break;
-      }
-      if (raise) {
+      if (softmax_any(need)) {
+        if (*reinterpret_cast<volatile int*>(&sm.abort_tile) <= n) {
+          aborted = true;
+          break;
+        }
         // A cached row that holds a NaN makes its whole column of S NaN.  Who
         // sees it gets NaN through P; for those that do not, 0 x NaN must not
         // reach O^T, so the row's values leave the tile.
@@ -709,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         }
         // O^T's columns lie across all four quadrants: each warp scales its lanes
         if (softmax_any(rescale) && n > 0) {
-          ok = wait_bar_warp(&sm.abort_flag, &sm.o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u, fw);
+          const int last = n - 1;  // its O^T must be done; this tile's waits for its P
+          ok = wait_bar_warp(&sm.abort_flag, &sm.free_[last % n_bufs], static_cast<uint32_t>(last / n_bufs) & 1u, fw);
           if (!ok) atomicMin(&sm.abort_tile, n + 1);
           tcgen05_fence_after();
           if (ok) {
