@@ -413,6 +413,9 @@ def mla_indexer_topk(q_idx, head_w, idx_key_pool, idx_block_stride, num_blocks, 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 def _here(*tensors) -> int:
     """The one device of `tensors` (None left out), which has to be the current one."""
     device = torch.cuda.current_device()
@@ -605,6 +608,7 @@ def mla_window_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, bloc
     q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
+    sinks, window = min(sinks, _INT_MAX), min(window, _INT_MAX)  # no context is longer
     if workspace is None:
         need = mla_window_decode_workspace_size(batch, q_len, heads, block_table.shape[1], sinks, window)
         workspace = _new(kv_pool, (need,), torch.uint8, stream) if need > 0 else None
@@ -633,6 +637,9 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
     q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
+    if prefix_len > _INT_MAX:
+        raise ValueError("prefix_len is a 32-bit length")
+    max_context_len = min(max_context_len, _INT_MAX)
     if prefix_len > 0:
         _here(out, prefix_table)
         if _contig(prefix_table, torch.int32, "prefix_table").numel() * block_size < prefix_len:
