@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "mla_device.cuh"
@@ -32,14 +33,24 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRing = 4;  // rows of a lane group in shared memory: one in work, three on their way
 constexpr int kPairs = kRope / 2;
-constexpr int kHeadCtas = 3;  // resident per SM (2: 34.9, 4, with spills: 38.5 us for 6,000 tokens x 32 heads x 192; 3: 33.3)
+constexpr int kHeadCtas = 3;  // resident per SM: at 4 the registers spill
 constexpr int kKvCtasPerSm = 6;
-constexpr int kHeadsPerTask = 4;  // consecutive (token, head) rows of one lane group
 
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 4-byte copy, and this thread's copies as groups of which all but the last N have come.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
@@ -91,56 +102,73 @@ __device__ __forceinline__ uint4 load_again(const uint4* p) {
 // at most), 128 contiguous bytes a load.  The rotated part is 8 consecutive
 // chunks, so every lane has exactly one of them, chunk (l - offset / 8) % 8 of
 // the part, and half-split pairs lie in lanes l and l ^ 4.  A lane group takes
-// kHeadsPerTask consecutive (token, head) rows: the angles of a token are
-// computed once for up to that many of its heads, and 4 heads share each
-// instruction.
+// `per` consecutive (token, head) rows and computes the angles of a token once
+// for those of its heads that are among them; 4 heads share each instruction.
+// Each thread copies its own chunks of the next three rows into shared memory
+// while it works on one: 3 CTAs of 256 threads then have 110 KB of reads in
+// flight on an SM.  With one row ahead in registers it was 37 KB, and the pass
+// over 6,000 tokens x 32 heads x 192 took 33.1 us, now 29.0 (147 MB: 5,080
+// GB/s; three rows in all 33.5, six 34.4, and 2 or 4 CTAs 29.2 and 36.7).
 template <int C>
 __device__ __forceinline__ void norm_rope_heads(const NormRopeArgs& a, const HeadSet& hs, int64_t task,
-                                                const uint64_t* turns) {
+                                                int per, const uint64_t* turns) {
+  extern __shared__ uint4 s_rows[];  // [kRing][C][threads]: each thread's own chunks, then [kRing][threads] positions
+  int* const s_pos = reinterpret_cast<int*>(s_rows + kRing * C * kThreads);
   const int gl = threadIdx.x & 7;
   const int64_t rows = a.tokens * hs.heads;
-  const int64_t r0 = task * kHeadsPerTask;
+  const int64_t r0 = task * per;
+  const int left = static_cast<int>(min(max(rows - r0, static_cast<int64_t>(0)), static_cast<int64_t>(per)));
   const int chunks = a.dim / 8;
   const int off = a.rope_offset / 8;
   const int rc = (gl - off) & 7;              // this lane's chunk within the rotated part
   const int c_rope = (off + rc - gl) / 8;     // and among its own
-  int64_t tok = rows <= 0x7FFFFFFF ? static_cast<uint32_t>(r0) / static_cast<uint32_t>(hs.heads) : r0 / hs.heads;
-  int head = static_cast<int>(r0 - tok * hs.heads);
-  const uint16_t* in = hs.in + tok * hs.in_token + head * hs.in_head + 8 * gl;
-  uint16_t* out = hs.out + tok * hs.out_token + head * hs.out_head + 8 * gl;
-  const int64_t in_wrap = hs.in_token - (hs.heads - 1) * hs.in_head;
-  const int64_t out_wrap = hs.out_token - (hs.heads - 1) * hs.out_head;
-  uint4 next[C];
-  auto load = [&](bool in_range) {
+  const int64_t tok0 = rows <= 0x7FFFFFFF ? static_cast<uint32_t>(r0) / static_cast<uint32_t>(hs.heads) : r0 / hs.heads;
+  int head = static_cast<int>(r0 - tok0 * hs.heads), in_head = head;
+  const uint16_t* in = hs.in + tok0 * hs.in_token + head * hs.in_head + 8 * gl;
+  uint16_t* out = hs.out + tok0 * hs.out_token + head * hs.out_head + 8 * gl;
+  const int32_t* pos = a.positions + tok0;
+  // row i on its way into the ring, and its token's position with the first of
+  // the token's rows
+  auto issue = [&](int i) {
+    if (i < left) {
+      const int slot = i % kRing;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      next[c] = in_range && gl + 8 * c < chunks ? *reinterpret_cast<const uint4*>(in + 64 * c) : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < C; ++c)
+        cp_async16(s_rows + (slot * C + c) * kThreads + threadIdx.x, in + (gl + 8 * c < chunks ? 64 * c : 0),
+                   gl + 8 * c < chunks ? 16 : 0);
+      if (i == 0 || in_head == 0) cp_async4(s_pos + slot * kThreads + threadIdx.x, pos);
+      const bool wrap = ++in_head == hs.heads;
+      in += wrap ? hs.in_token - (hs.heads - 1) * hs.in_head : hs.in_head;
+      pos += wrap;
+      in_head = wrap ? 0 : in_head;
+    }
+    cp_async_commit();
   };
-  load(r0 < rows);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
   const float inv_dim = 1.f / static_cast<float>(a.dim);
-  bool fresh = true;  // the angles are another token's
   float sn[4], cs[4];  // interleaved: this chunk's pairs; else half of them, the other half is the partner's
 #pragma unroll 1
-  for (int i = 0; i < kHeadsPerTask; ++i) {
-    const bool here = r0 + i < rows;  // uniform over the lane group
+  for (int i = 0; i < per; ++i) {
+    const bool here = i < left;  // uniform over the lane group
+    const int slot = i % kRing;
+    cp_async_wait<kRing - 2>();  // row i has come
     F2 v[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      v[c][0] = bf16x2_floats(next[c].x);
-      v[c][1] = bf16x2_floats(next[c].y);
-      v[c][2] = bf16x2_floats(next[c].z);
-      v[c][3] = bf16x2_floats(next[c].w);
+      const uint4 x = s_rows[(slot * C + c) * kThreads + threadIdx.x];
+      v[c][0] = bf16x2_floats(x.x);
+      v[c][1] = bf16x2_floats(x.y);
+      v[c][2] = bf16x2_floats(x.z);
+      v[c][3] = bf16x2_floats(x.w);
     }
-    const int64_t now = tok;
-    const bool first = fresh;
+    const bool first = i == 0 || head == 0;  // the angles are another token's
+    const int at = s_pos[slot * kThreads + threadIdx.x];
     uint16_t* const dst = out;
     const bool wrap = ++head == hs.heads;
-    in += wrap ? in_wrap : hs.in_head;
-    out += wrap ? out_wrap : hs.out_head;
+    out += wrap ? hs.out_token - (hs.heads - 1) * hs.out_head : hs.out_head;
     head = wrap ? 0 : head;
-    tok += wrap;
-    fresh = wrap;
-    if (i + 1 < kHeadsPerTask) load(r0 + i + 1 < rows);
+    issue(i + kRing - 1);
     if (hs.weight != nullptr) {
       F2 ss = {0.f, 0.f};
 #pragma unroll
@@ -164,10 +192,9 @@ __device__ __forceinline__ void norm_rope_heads(const NormRopeArgs& a, const Hea
       }
     }
     if (first && here) {
-      const int pos = __ldg(a.positions + now);
       const int p0 = a.interleaved ? 4 * rc : 8 * (rc & 3) + (rc & 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) angle(turns[p0 + k], pos, &sn[k], &cs[k]);
+      for (int k = 0; k < 4; ++k) angle(turns[p0 + k], at, &sn[k], &cs[k]);
     }
     F2 r[4];
 #pragma unroll
@@ -283,7 +310,7 @@ __device__ __forceinline__ void norm_rope_append_rows(const NormRopeArgs& a, int
 // CTAs [0, kv_ctas) take latent rows, the others tasks of the two head sets.
 template <int C, int FMT>
 __global__ void __launch_bounds__(kWarps * 32, kHeadCtas)
-    norm_rope_kernel(const NormRopeArgs a, unsigned kv_ctas, int64_t q_tasks, int64_t tasks) {
+    norm_rope_kernel(const NormRopeArgs a, unsigned kv_ctas, int per, int64_t q_tasks, int64_t tasks) {
   __shared__ uint64_t turns[kPairs];
   if (threadIdx.x < kPairs) {
     // inv_freq / 2 pi of a turn, as a fraction of 2^64
@@ -304,42 +331,63 @@ __global__ void __launch_bounds__(kWarps * 32, kHeadCtas)
     if (warp_first >= tasks) return;
     // q_tasks is a multiple of the tasks per warp, so a warp has one set
     const bool is_k = warp_first >= q_tasks;
-    norm_rope_heads<C>(a, a.set[is_k], task - (is_k ? q_tasks : 0), turns);
+    norm_rope_heads<C>(a, a.set[is_k], task - (is_k ? q_tasks : 0), per, turns);
   }
 }
 
 template <int C>
-cudaError_t launch_chunks(const NormRopeArgs& a, unsigned grid, unsigned kv_ctas, int64_t q_tasks, int64_t tasks,
+cudaError_t launch_chunks(const NormRopeArgs& a, unsigned grid, unsigned kv_ctas, int per, int64_t q_tasks, int64_t tasks,
                          cudaStream_t stream) {
-  auto* kernel = a.kv == nullptr ? norm_rope_kernel<C, -1> : a.fmt == 0 ? norm_rope_kernel<C, 0> : norm_rope_kernel<C, 1>;
-  kernel<<<grid, kWarps * 32, 0, stream>>>(a, kv_ctas, q_tasks, tasks);
+  static std::atomic<uint64_t> configured[3];
+  const int which = a.kv == nullptr ? 0 : a.fmt == 0 ? 1 : 2;
+  auto* kernel = which == 0 ? norm_rope_kernel<C, -1> : which == 1 ? norm_rope_kernel<C, 0> : norm_rope_kernel<C, 1>;
+  constexpr int kSmem = C == 0 ? 0 : kRing * kThreads * (C * 16 + 4);
+  if (kSmem > 0) {
+    const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), kSmem, &configured[which]);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, kThreads, kSmem, stream>>>(a, kv_ctas, per, q_tasks, tasks);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  int64_t set_tasks[2];
-  for (int i = 0; i < 2; ++i) {
-    const int64_t rows = a.set[i].in != nullptr ? a.tokens * a.set[i].heads : 0;
-    set_tasks[i] = ((rows + kHeadsPerTask - 1) / kHeadsPerTask + 3) / 4 * 4;  // whole warps
-  }
-  const int64_t tasks = set_tasks[0] + set_tasks[1];
-  // latent rows: at most kKvCtasPerSm CTAs per SM, whose warps stride over them
+  const int64_t sms = device_sm_count();
+  int64_t rows[2], set_tasks[2];
+  for (int i = 0; i < 2; ++i) rows[i] = a.set[i].in != nullptr ? a.tokens * a.set[i].heads : 0;
+  const int64_t head_rows = rows[0] + rows[1];
+  // latent rows: warps that stride over them; beside heads, in a share of the
+  // resident CTAs that is their share of the bytes
   const int64_t kv_want = a.kv != nullptr ? (a.tokens + kWarps - 1) / kWarps : 0;
-  const int64_t kv_cap = static_cast<int64_t>(device_sm_count()) * kKvCtasPerSm;
+  int64_t kv_cap = sms * kKvCtasPerSm;
+  if (head_rows > 0) {
+    const double kv_bytes = static_cast<double>(a.tokens) * ((kLatent + kRope) * 2 + (a.fmt == 0 ? kRowNvfp4 : kRowFp8));
+    const double head_bytes = static_cast<double>(head_rows) * a.dim * 4;
+    kv_cap = static_cast<int64_t>(sms * kHeadCtas * (kv_bytes / (kv_bytes + head_bytes))) + 1;
+  }
   const int64_t kv_ctas = kv_want < kv_cap ? kv_want : kv_cap;
+  // Rows per lane group: all groups resident at once, so that no wave is partly
+  // filled, and one row each while they are few (64 tokens x 33 heads: 4.1 us,
+  // 5.6 with 4 rows each).
+  const int64_t room = sms * kHeadCtas - kv_ctas;
+  const int64_t groups = (room > 1 ? room : 1) * (kWarps * 4);
+  const int64_t per = head_rows > groups ? (head_rows + groups - 1) / groups : 1;
+  for (int i = 0; i < 2; ++i) set_tasks[i] = ((rows[i] + per - 1) / per + 3) / 4 * 4;  // whole warps
+  const int64_t tasks = set_tasks[0] + set_tasks[1];
   const int64_t head_ctas = (tasks * 8 + kWarps * 32 - 1) / (kWarps * 32);
   const int64_t grid = kv_ctas + head_ctas;
   if (grid == 0) return cudaSuccess;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (per > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned g = static_cast<unsigned>(grid), k = static_cast<unsigned>(kv_ctas);
+  const int p = static_cast<int>(per);
   switch (tasks == 0 ? 0 : (a.dim + 63) / 64) {  // 8-value chunks per lane
-    case 0: return launch_chunks<0>(a, g, k, set_tasks[0], tasks, stream);
-    case 1: return launch_chunks<1>(a, g, k, set_tasks[0], tasks, stream);
-    case 2: return launch_chunks<2>(a, g, k, set_tasks[0], tasks, stream);
-    case 3: return launch_chunks<3>(a, g, k, set_tasks[0], tasks, stream);
-    default: return launch_chunks<4>(a, g, k, set_tasks[0], tasks, stream);
+    case 0: return launch_chunks<0>(a, g, k, p, set_tasks[0], tasks, stream);
+    case 1: return launch_chunks<1>(a, g, k, p, set_tasks[0], tasks, stream);
+    case 2: return launch_chunks<2>(a, g, k, p, set_tasks[0], tasks, stream);
+    case 3: return launch_chunks<3>(a, g, k, p, set_tasks[0], tasks, stream);
+    default: return launch_chunks<4>(a, g, k, p, set_tasks[0], tasks, stream);
   }
 }
 
