@@ -15,19 +15,26 @@
 // Work split.  One CTA = 64 columns x a slice of their tiles; slices' partial
 // outputs (normalised, f16) and base-2 LSEs are joined by dense_merge_kernel.
 // Roles: one lane issues every tcgen05.mma; one copies each tile, which is
-// contiguous, with one bulk copy; two sets of 4 warps unpack tiles in turn; 4
-// warps run the softmax, 16 columns each; all write the output.  The unpacked
-// tile is stored once, as 8 x 8 core matrices, dim group major, which is at the
-// same time the K-major B operand of S (N = 32 rows) and the MN-major A operand
-// of O^T (M = 128 dims).  P lies in the tile's rope part, which only S reads.
+// contiguous, with one bulk copy; 8 warps unpack a tile (8 rows x half the dims
+// each); 8 run its softmax (16 columns x 16 rows each); all write the output.
+// The unpacked tile is stored once, as 8 x 8 core matrices, dim group major,
+// which is at the same time the K-major B operand of S (N = 32 rows) and the
+// MN-major A operand of O^T (M = 128 dims).  P lies in the tile's rope part,
+// which only S reads.
 //
-// What bounds it.  Both products read their operands from shared memory at its
-// full rate (S: 36 MMAs of ~24 cycles, O^T: 8 of ~48 per tile), and each tile
-// is a chain of hand-offs -- copy, unpack, S, softmax, O^T -- of several hundred
-// cycles each.  What hides the chain is tiles in flight: S of the next tile is
-// issued before O^T of this one.  32 rows and not 64 or 128, so that three
-// unpacked tiles (37 KB each) fit beside a 72 KB query; at 64 rows only pieces
-// of the next tile did.
+// What bounds it.  A tile's chain of hand-offs -- copy, unpack, S, softmax, O^T
+// -- is ~5,000 cycles long for any number of columns, and the tiles in flight
+// hide it as far as they go: a tile every ~1,700 cycles, against ~1,250 of the
+// tensor core, whose operands come from shared memory at its full rate (S: 36
+// MMAs of ~24 cycles, O^T: 8 of ~48).  S of the next tile is issued before O^T
+// of this one, and the softmax and the issuing lane take equally long: halving
+// either alone changes nothing.  32 rows a tile and not 64 or 128, so that three
+// unpacked tiles (37 KB each) fit beside a 72 KB query of 64 columns; pieces of
+// 64-row tiles took 204 us where this takes 118 (128 requests x 64 heads, window
+// 4,096), 64-row tiles beside 16 columns 81 us where this takes 64.5 (32
+// requests, window 8,192).  Slower as well: S two tiles ahead, an issuing lane
+// for each product, two softmax sets on tiles in turn, and S of the next tile
+// loaded while P is computed -- each delays O^T, which frees the tile.
 //
 // Every wait is bounded; one that runs out sets the library's fault bit and
 // the CTA leaves after its copies and MMAs in flight have drained.

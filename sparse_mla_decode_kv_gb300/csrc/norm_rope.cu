@@ -19,7 +19,9 @@
 //
 // Bound: HBM, 4 bytes per query / key value; per latent row 1,152 bytes and 12
 // of slot and position in, 352 (NVFP4) or 576 (FP8) out, where a norm pass
-// followed by the quantize-on-write pass would move 2,304 bytes more.
+// followed by the quantize-on-write pass would move 2,304 bytes more.  384,000
+// FP8 rows: 123 us, 5,430 GB/s; a second row ahead gains nothing there (124.6),
+// nor do more CTAs (48 registers, with spills: 173 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,8 +38,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 4;  // rows of a lane group in shared memory: one in work, three on their way
 constexpr int kPairs = kRope / 2;
-constexpr int kHeadCtas = 3;  // resident per SM: at 4 the registers spill
-constexpr int kKvCtasPerSm = 6;
+constexpr int kCtasPerSm = 3;  // resident per SM: at 4 the registers spill
 
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -309,7 +310,7 @@ __device__ __forceinline__ void norm_rope_append_rows(const NormRopeArgs& a, int
 
 // CTAs [0, kv_ctas) take latent rows, the others tasks of the two head sets.
 template <int C, int FMT>
-__global__ void __launch_bounds__(kWarps * 32, kHeadCtas)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     norm_rope_kernel(const NormRopeArgs a, unsigned kv_ctas, int per, int64_t q_tasks, int64_t tasks) {
   __shared__ uint64_t turns[kPairs];
   if (threadIdx.x < kPairs) {
@@ -360,17 +361,17 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   // latent rows: warps that stride over them; beside heads, in a share of the
   // resident CTAs that is their share of the bytes
   const int64_t kv_want = a.kv != nullptr ? (a.tokens + kWarps - 1) / kWarps : 0;
-  int64_t kv_cap = sms * kKvCtasPerSm;
+  int64_t kv_cap = sms * kCtasPerSm;
   if (head_rows > 0) {
     const double kv_bytes = static_cast<double>(a.tokens) * ((kLatent + kRope) * 2 + (a.fmt == 0 ? kRowNvfp4 : kRowFp8));
     const double head_bytes = static_cast<double>(head_rows) * a.dim * 4;
-    kv_cap = static_cast<int64_t>(sms * kHeadCtas * (kv_bytes / (kv_bytes + head_bytes))) + 1;
+    kv_cap = static_cast<int64_t>(sms * kCtasPerSm * (kv_bytes / (kv_bytes + head_bytes))) + 1;
   }
   const int64_t kv_ctas = kv_want < kv_cap ? kv_want : kv_cap;
   // Rows per lane group: all groups resident at once, so that no wave is partly
   // filled, and one row each while they are few (64 tokens x 33 heads: 4.1 us,
   // 5.6 with 4 rows each).
-  const int64_t room = sms * kHeadCtas - kv_ctas;
+  const int64_t room = sms * kCtasPerSm - kv_ctas;
   const int64_t groups = (room > 1 ? room : 1) * (kWarps * 4);
   const int64_t per = head_rows > groups ? (head_rows + groups - 1) / groups : 1;
   for (int i = 0; i < 2; ++i) set_tasks[i] = ((rows[i] + per - 1) / per + 3) / 4 * 4;  // whole warps
