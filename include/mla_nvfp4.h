@@ -516,7 +516,8 @@ mla_status_t mla_kv_norm_rope_append(const uint16_t* kv, int64_t kv_token_stride
  *   lse           device float [batch, q_len, num_heads], or NULL
  *   workspace     at least mla_window_decode_workspace_size(...) bytes,
  *                 256-byte aligned (that size depends on the current device
- *                 and may be 0); contents on entry do not matter
+ *                 and may be 0); contents on entry do not matter; calls that
+ *                 may run at the same time need one each
  * All other arguments as for mla_sparse_decode.  batch == 0 is a no-op.
  */
 size_t mla_window_decode_workspace_size(int batch, int q_len, int num_heads, int max_blocks_per_req, int sinks,

@@ -198,3 +198,35 @@ def test_captured_step_replays_like_the_eager_one(m, fmt):
         for name in ("table", "ctx", "state", "pool"):
             assert torch.equal(getattr(s, name), getattr(eager, name)), (i, name)
     assert m.mla_device_fault() == 0
+
+
+def test_two_graphs_share_a_workspace_in_turn(m):
+    """Captured calls of different shapes on one workspace: what one leaves in it does not reach the other."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    blocks = 80
+    pool = torch.randint(0, 0x70, (blocks, 64 * 576), generator=g, device=DEV).to(torch.uint8)  # finite e4m3
+    table = torch.randperm(blocks, generator=g, device=DEV).to(torch.int32).view(2, 40)
+    ctx = torch.tensor([2500, 900], dtype=torch.int32, device=DEV)
+    qs = [torch.randn((2, n, HEADS, 576), generator=g, device=DEV).to(torch.bfloat16) for n in (1, 3)]
+    args = [(q[..., :512].contiguous(), q[..., 512:].contiguous(), pool, 64 * 576, blocks) for q in qs]
+    calls = [
+        lambda **kw: m.mla_window_decode(*args[0], table, ctx, SCALE / 64, 2, 2000, fmt=1, **kw),
+        lambda **kw: m.mla_prefix_decode(*args[1], table[0], 700, table, ctx, SCALE / 64, 2560, fmt=1, **kw),
+    ]
+    want = [c()[0].clone() for c in calls]
+    need = max(m.mla_window_decode_workspace_size(2, 1, HEADS, 40, 2, 2000),
+               m.mla_prefix_decode_workspace_size(2, 3, HEADS, 700, 40, 2560))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN where nothing was written
+    outs = [torch.empty_like(w) for w in want]
+    graphs = []
+    for c, o in zip(calls, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c(out=o, workspace=ws)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want[i]), i
+    assert m.mla_device_fault() == 0
