@@ -496,20 +496,31 @@ def mla_block_table_extend(context_lens, new_lens, block_table, free_blocks, fre
     return slot_mapping, positions, query_start, context_lens_out, free_state_out
 
 
+def _head_strides(x, what):
+    """Token and head stride of bf16 heads [n, H, D] whose last axis is contiguous."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: expected torch.bfloat16, got {x.dtype}")
+    strides = x.stride()
+    if len(strides) != 3 or (strides[2] != 1 and x.numel() > 0):
+        raise ValueError(f"{what} must be [n, heads, dim] with a contiguous last axis")
+    return strides
+
+
 def _heads(x, weight, out, name, stream):
-    """(mla_heads_t, output) of bf16 heads [n, H, D] whose last axis is contiguous."""
-    for t, what in ((x, name), (out, name + "_out")):
-        if t is None:
-            continue
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{what}: expected torch.bfloat16, got {t.dtype}")
-        if t.dim() != 3 or t.shape != x.shape or (t.numel() > 0 and t.stride(2) != 1):
-            raise ValueError(f"{what} must be [n, heads, dim] with a contiguous last axis, out shaped like in")
-    if weight is not None and _contig(weight, torch.bfloat16, name + "_weight").numel() != x.shape[2]:
-        raise ValueError(f"{name}_weight must have one value for each of {x.shape[2]} dims")
+    """(mla_heads_t, output) of the heads x."""
+    in_token, in_head, _ = _head_strides(x, name)
+    shape = x.shape
+    _, heads, dim = shape
+    if weight is not None and _contig(weight, torch.bfloat16, name + "_weight").numel() != dim:
+        raise ValueError(f"{name}_weight must have one value for each of {dim} dims")
     if out is None:
-        out = _new(x, x.shape, torch.bfloat16, stream)
-    return _Heads(x.data_ptr(), out.data_ptr(), x.shape[1], x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+        out = _new(x, shape, torch.bfloat16, stream)
+        out_token, out_head = heads * dim, dim
+    else:
+        if out.shape != shape:
+            raise ValueError(f"{name}_out must be shaped like {name}")
+        out_token, out_head, _ = _head_strides(out, name + "_out")
+    return _Heads(x.data_ptr(), out.data_ptr(), heads, in_token, in_head, out_token, out_head,
                   None if weight is None else weight.data_ptr()), out
 
 
@@ -527,16 +538,17 @@ def mla_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     and heads; positions int32 [n]; inv_freq float64 [32].  Returns (q_out,
     k_out or None); q_out may be q, k_out may be k."""
     device = _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    _angles(positions, inv_freq, q.shape[0])
-    if k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
-        raise ValueError("q and k must have the same tokens and head dim")
     hq, q_out = _heads(q, q_weight, q_out, "q", stream)
+    n, _, dim = q.shape
+    _angles(positions, inv_freq, n)
     hk = None
     if k is not None:
         hk, k_out = _heads(k, k_weight, k_out, "k", stream)
+        if k.shape[0] != n or k.shape[2] != dim:
+            raise ValueError("q and k must have the same tokens and head dim")
     _check("mla_qk_norm_rope",
-           load().mla_qk_norm_rope(C.byref(hq), None if hk is None else C.byref(hk), q.shape[0], q.shape[2],
-                                   rope_offset, int(interleaved), float(eps), _at(positions), _at(inv_freq),
+           load().mla_qk_norm_rope(C.byref(hq), None if hk is None else C.byref(hk), n, dim, rope_offset,
+                                   int(interleaved), float(eps), _at(positions), _at(inv_freq),
                                    _on(stream, device)))
     return q_out, (None if k is None else k_out)
 
