@@ -578,8 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       uint2 rope = *reinterpret_cast<const uint2*>(row + (FMT == 0 ? kRopeOffNvfp4 : kRopeOffFp8) + 32 * half +
                                                    8 * quarter);
       if (!seen) rope = make_uint2(0, 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.raw_free[slot]);  // the copy has been read
+      // The copy has been read.  The next one writes the slot through another
+      // proxy, so each lane's reads are fenced: without it they may still be on
+      // their way, behind the tensor core's reads, when that copy lands.
+      warp_publish(&sm.raw_free[slot], lane);
       if (n >= n_bufs) ok = wait_bar_warp(&sm.abort_flag, &sm.free_[buf], free_phase, fw);
       if (!ok) break;
 #pragma unroll

@@ -230,3 +230,30 @@ def test_two_graphs_share_a_workspace_in_turn(m):
         torch.cuda.synchronize()
         assert torch.equal(outs[i], want[i]), i
     assert m.mla_device_fault() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (48, 1), (48, 2), (64, 4)])
+def test_many_calls_in_a_row(m, fmt, heads, q_len):
+    """Calls queued without a pause give what each gives alone: the rows come from L2 and every ring of copies
+    and tiles runs at its fastest."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(heads + q_len)
+    batch, width = 20, 63
+    rb = ROW_BYTES[fmt]
+    pool = torch.randint(0, 0x70, (batch * width, 64 * rb), generator=g, device=DEV).to(torch.uint8)
+    table = torch.randperm(batch * width, generator=g, device=DEV).to(torch.int32).view(batch, width)
+    ctx = torch.randint(0, 4000, (batch,), generator=g, device=DEV).to(torch.int32)
+    q = torch.randn((batch, q_len, heads, 576), generator=g, device=DEV).to(torch.bfloat16) / 64
+    qn, qr = q[..., :512].contiguous(), q[..., 512:].contiguous()
+
+    def call():
+        return m.mla_window_decode(qn, qr, pool, 64 * rb, batch * width, table, ctx, SCALE, 7, 1500, fmt=fmt)[0]
+
+    want = call()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        got = [call() for _ in range(24)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in got)
+    assert m.mla_device_fault() == 0
