@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     // 16-byte stores out); every load is issued before the first is used.  A
     // column whose query holds an infinity or NaN enters as zeros with a NaN
     // scale: its results are NaN, its neighbours' are not.
+    // Coherent loads, as an earlier call's output may be the query.
     constexpr int kPieces = kDimGroups / 4;               // of 32 dims
     constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 9
     const int n_tasks = (u.ncols / 8) * kPieces;
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       x[i] = make_uint4(0, 0, 0, 0);
       if (task < n_tasks)
         x[i] = dg < kLatent / 8
-                   ? __ldg(reinterpret_cast<const uint4*>(args.q_nope + col * kLatent) + dg)
-                   : __ldg(reinterpret_cast<const uint4*>(args.q_rope + col * kRope) + (dg - kLatent / 8));
+                   ? __ldcg(reinterpret_cast<const uint4*>(args.q_nope + col * kLatent) + dg)
+                   : __ldcg(reinterpret_cast<const uint4*>(args.q_rope + col * kRope) + (dg - kLatent / 8));
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -828,6 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
 // O_s.  One CTA per column, four dims per thread; the loads of a chunk of
 // partials are all issued before the first is used.  A partial whose LSE is
 // -inf was not written and is not read.
+// Coherent loads from L2: this grid may be resident before the partials are
+// written, which the read-only path does not allow.
 constexpr int kMergeChunk = 8;
 __global__ void __launch_bounds__(128) dense_merge_kernel(const __half* __restrict__ part_o,
                                                           const float* __restrict__ part_lse, int parts,
@@ -844,10 +847,10 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __half* __restri
     float ls[kMergeChunk];
     uint2 v[kMergeChunk];
 #pragma unroll
-    for (int i = 0; i < kMergeChunk; ++i) ls[i] = s0 + i < parts ? __ldg(pl + s0 + i) : -INFINITY;
+    for (int i = 0; i < kMergeChunk; ++i) ls[i] = s0 + i < parts ? __ldcg(pl + s0 + i) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < kMergeChunk; ++i)
-      v[i] = ls[i] != -INFINITY ? __ldg(src + static_cast<int64_t>(s0 + i) * (kLatent / 4)) : make_uint2(0, 0);
+      v[i] = ls[i] != -INFINITY ? __ldcg(src + static_cast<int64_t>(s0 + i) * (kLatent / 4)) : make_uint2(0, 0);
     float cm = mx;
 #pragma unroll
     for (int i = 0; i < kMergeChunk; ++i) cm = ls[i] > cm || isnan(ls[i]) ? ls[i] : cm;
