@@ -108,11 +108,12 @@ __device__ __forceinline__ uint4 load_again(const uint4* p) {
 // Each thread copies its own chunks of the next three rows into shared memory
 // while it works on one: 3 CTAs of 256 threads then have 110 KB of reads in
 // flight on an SM.  With one row ahead in registers it was 37 KB, and the pass
-// over 6,000 tokens x 32 heads x 192 took 33.1 us, now 29.0 (147 MB: 5,080
-// GB/s; three rows in all 33.5, six 34.4, and 2 or 4 CTAs 29.2 and 36.7).
-template <int C>
+// over 6,000 tokens x 32 heads x 192 took 33.1 us, then 29.0 (three rows in all
+// 33.5, five 29.9, six 34.4; 2 or 4 CTAs 29.2 and 36.7), and 28.2 (147 MB: 5,230
+// GB/s) with the first rows on their way before the angles are set up.
+template <int C, typename F>
 __device__ __forceinline__ void norm_rope_heads(const NormRopeArgs& a, const HeadSet& hs, int64_t task,
-                                                int per, const uint64_t* turns) {
+                                                int per, const uint64_t* turns, const F& set_turns) {
   extern __shared__ uint4 s_rows[];  // [kRing][C][threads]: each thread's own chunks, then [kRing][threads] positions
   int* const s_pos = reinterpret_cast<int*>(s_rows + kRing * C * kThreads);
   const int gl = threadIdx.x & 7;
@@ -147,6 +148,7 @@ __device__ __forceinline__ void norm_rope_heads(const NormRopeArgs& a, const Hea
   };
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) issue(i);
+  set_turns();
   const float inv_dim = 1.f / static_cast<float>(a.dim);
   float sn[4], cs[4];  // interleaved: this chunk's pairs; else half of them, the other half is the partner's
 #pragma unroll 1
@@ -245,14 +247,13 @@ struct LatentRow {
   uint32_t p, q;
   int pos;
 };
-template <int FMT>
+template <int FMT, typename F>
 __device__ __forceinline__ void norm_rope_append_rows(const NormRopeArgs& a, int64_t first, int64_t stride,
-                                                      const uint64_t* turns) {
+                                                      const uint64_t* turns, const F& set_turns) {
   const int lane = threadIdx.x & 31;
   const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(a.latent_weight + lane * kGroup));
   const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(a.latent_weight + lane * kGroup) + 1);
   const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  const uint64_t turn = turns[lane];
   const int e0 = a.interleaved ? 2 * lane : lane, e1 = a.interleaved ? 2 * lane + 1 : lane + kPairs;
   auto load = [&](int64_t n) {
     LatentRow r;
@@ -269,6 +270,8 @@ __device__ __forceinline__ void norm_rope_append_rows(const NormRopeArgs& a, int
     return r;
   };
   LatentRow next = load(first);
+  set_turns();
+  const uint64_t turn = turns[lane];
   for (int64_t n = first; n < a.tokens; n += stride) {
     const LatentRow r = next;
     next = load(n + stride);
@@ -313,15 +316,18 @@ template <int C, int FMT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     norm_rope_kernel(const NormRopeArgs a, unsigned kv_ctas, int per, int64_t q_tasks, int64_t tasks) {
   __shared__ uint64_t turns[kPairs];
-  if (threadIdx.x < kPairs) {
-    // inv_freq / 2 pi of a turn, as a fraction of 2^64
-    const double f = a.inv_freq[threadIdx.x] * 0.15915494309189535;
-    turns[threadIdx.x] = static_cast<uint64_t>((f - floor(f)) * 18446744073709551616.0);
-  }
-  __syncthreads();
+  // Every thread calls this once, after it has started its first loads.
+  const auto set_turns = [&] {
+    if (threadIdx.x < kPairs) {
+      // inv_freq / 2 pi of a turn, as a fraction of 2^64
+      const double f = a.inv_freq[threadIdx.x] * 0.15915494309189535;
+      turns[threadIdx.x] = static_cast<uint64_t>((f - floor(f)) * 18446744073709551616.0);
+    }
+    __syncthreads();
+  };
   if (FMT >= 0 && blockIdx.x < kv_ctas) {
     norm_rope_append_rows<FMT>(a, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
-                               static_cast<int64_t>(kv_ctas) * kWarps, turns);
+                               static_cast<int64_t>(kv_ctas) * kWarps, turns, set_turns);
     return;
   }
   if constexpr (C > 0) {
@@ -329,10 +335,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     const int64_t task = (cta * (kWarps * 32) + threadIdx.x) / 8;
     // whole warps stay together: the shuffles name every lane
     const int64_t warp_first = (cta * (kWarps * 32) + (threadIdx.x & ~31u)) / 8;
-    if (warp_first >= tasks) return;
+    if (warp_first >= tasks) {
+      set_turns();
+      return;
+    }
     // q_tasks is a multiple of the tasks per warp, so a warp has one set
     const bool is_k = warp_first >= q_tasks;
-    norm_rope_heads<C>(a, a.set[is_k], task - (is_k ? q_tasks : 0), per, turns);
+    norm_rope_heads<C>(a, a.set[is_k], task - (is_k ? q_tasks : 0), per, turns, set_turns);
   }
 }
 
@@ -369,8 +378,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   }
   const int64_t kv_ctas = kv_want < kv_cap ? kv_want : kv_cap;
   // Rows per lane group: all groups resident at once, so that no wave is partly
-  // filled, and one row each while they are few (64 tokens x 33 heads: 4.1 us,
-  // 5.6 with 4 rows each).
+  // filled, and one row each while they are few (64 tokens x 33 heads: 3.6 us;
+  // with 4 rows each 5.6 where this was 4.2).
   const int64_t room = sms * kCtasPerSm - kv_ctas;
   const int64_t groups = (room > 1 ? room : 1) * (kWarps * 4);
   const int64_t per = head_rows > groups ? (head_rows + groups - 1) / groups : 1;
