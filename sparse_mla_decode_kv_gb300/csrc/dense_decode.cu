@@ -22,19 +22,18 @@
 // MN-major A operand of O^T (M = 128 dims).  P lies in the tile's rope part,
 // which only S reads.
 //
-// What bounds it.  A tile's chain of hand-offs -- copy, unpack, S, softmax, O^T
-// -- is ~5,000 cycles long for any number of columns, and the tiles in flight
-// hide it as far as they go: a tile every ~1,700 cycles, against ~1,250 of the
-// tensor core, whose operands come from shared memory at its full rate (S: 36
-// MMAs of ~24 cycles, O^T: 8 of ~48).  S of the next tile is issued before O^T
-// of this one, and the softmax and the issuing lane take equally long: halving
-// either alone changes nothing.  32 rows a tile and not 64 or 128, so that three
-// unpacked tiles (37 KB each) fit beside a 72 KB query of 64 columns; pieces of
-// 64-row tiles took 204 us where this takes 118 (128 requests x 64 heads, window
-// 4,096), 64-row tiles beside 16 columns 81 us where this takes 64.5 (32
-// requests, window 8,192).  Slower as well: S two tiles ahead, an issuing lane
-// for each product, two softmax sets on tiles in turn, and S of the next tile
-// loaded while P is computed -- each delays O^T, which frees the tile.
+// What bounds it.  No pipe is full: the issuing lane never waits, but a tile
+// costs it ~1,700 cycles, 820 of them for the 36 MMAs of S (~23 each, which is
+// also what their operands take from shared memory), 175 for the 8 of O^T (which
+// run ~48 each), the rest barriers, commits and the loop; the softmax's serial
+// part is as long, so halving either alone changes nothing.  S of the next tile
+// is issued before O^T of this one.  32 rows a tile and not 64 or 128, so that
+// three unpacked tiles (37 KB each) fit beside a 72 KB query of 64 columns:
+// pieces of 64-row tiles took 204 us where this takes 118 (128 requests x 64
+// heads, window 4,096), 64-row tiles beside 16 columns 68 to 81 us where this
+// takes 64 (32 requests, window 8,192).  Slower as well: S two tiles ahead, an
+// issuing lane for each product, two softmax sets on tiles in turn, and S of the
+// next tile loaded while P is computed -- each delays O^T, which frees the tile.
 //
 // Every wait is bounded; one that runs out sets the library's fault bit and
 // the CTA leaves after its copies and MMAs in flight have drained.
