@@ -6,7 +6,7 @@
 // same cached rows -- share one walk over those rows, half a cache block of 32
 // rows (one tile) at a time:
 //   S[64 columns x 32 rows] = Q[64 x 576] . K^T
-//   P = 2^(S scale - m), m the column's running maximum (raised lazily)
+//   P = 2^(S scale - r), r 9 below the column's running maximum (raised lazily)
 //   O^T[512 x 64] = O^T + V^T[512 x 32] . P^T,   V = the first 512 of K
 // and each column's denominator is summed in float beside it, so the rows are
 // read and unpacked once for all 64 columns.  A request's query tokens and
@@ -78,11 +78,16 @@ constexpr int kMaxTiles = 4;                          // unpacked tiles
 static_assert(kCols / 8 * kPGroupBytes <= kRope / 8 * kDgBytes, "P fits the rope part");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 64;  // S: columns 0-31 and 32-63 (tiles in turn), O^T: 64-319
-// The maximum of a column is raised only when a score exceeds it by 2^14: P
-// stays below f16's 65,504 at the same relative precision, and O^T is rarely
-// rescaled (at 2^8, 64 columns of scores with a deviation of 4 bits were in
-// every third tile: 128 x 64 heads, window 4,096: 131 us, now 118).
-constexpr float kLazyRaise = 14.f;
+// P is f16, which has its full precision from 2^-14 to 2^16.  A raise puts a
+// column's largest score so far at 2^9: a row keeps its weight to 2^-11 until it
+// is 2^23 below the largest, and further down loses at most 2^-34 of the largest
+// weight (with 10 instead of 9 2^24 and 2^-35, and 122.5 us where this takes 121:
+// 128 requests x 64 heads, window 4,096, scores with a deviation of 3 bits).
+// Scores that come later may reach 2^15.99 before the next raise, which, for
+// whichever column it is, brings all 64 to their maxima: raising only the columns
+// past the limit takes 155 us.
+constexpr float kRaiseTo = 9.f;
+constexpr float kRaiseAt = 15.99f;
 constexpr float kLn2f = 0.6931471805599453f;
 
 struct Ctl {              // the fixed part of shared memory, at its start
@@ -617,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     const bool has_cols = 16 * quad < u.ncols;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const int me = u.me0 + (u.tok_col0 + 16 * quad) / args.num_heads;  // 16 columns share a query token
-    float qs[2] = {0.f, 0.f}, mr[2] = {-INFINITY, -INFINITY};  // scale and (lazy) maximum, base 2
+    float qs[2] = {0.f, 0.f}, ref[2] = {-INFINITY, -INFINITY};  // scale and what P is relative to, base 2
+    float top[2] = {-INFINITY, -INFINITY};                      // largest scores of this thread's rows so far
     float l_part[2] = {0.f, 0.f};  // these rows' share of the denominators
     if (has_cols) {
       qs[0] = sm.qscale[col0];
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
       bool ok = wait_bar_warp(&sm.abort_flag, &sm.s_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, fw);
       tcgen05_fence_after();
       float z[8];  // [4 k + 2 c + e]: row 8 k + t_lane + e, column col0 + 8 c
-      float nan_sum = 0.f, top[2] = {-INFINITY, -INFINITY};
+      float nan_sum = 0.f;
       bool need = !ok;
       if (has_cols && ok) {
         uint32_t sr[8];
@@ -665,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          top[c] = fmaxf(fmaxf(z[2 * c], z[2 * c + 1]), fmaxf(z[4 + 2 * c], z[4 + 2 * c + 1]));
-        need = isnan(nan_sum) || top[0] > mr[0] + kLazyRaise || top[1] > mr[1] + kLazyRaise;
+          top[c] = fmaxf(top[c], fmaxf(fmaxf(z[2 * c], z[2 * c + 1]), fmaxf(z[4 + 2 * c], z[4 + 2 * c + 1])));
+        need = isnan(nan_sum) || top[0] > ref[0] + kRaiseAt || top[1] > ref[1] + kRaiseAt;
       }
       if (!ok) atomicMin(&sm.abort_tile, n);
       // every softmax thread takes the same branch at every barrier: a failed
@@ -700,23 +706,22 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
           if ((lane & 3) == 0) sm.part[rh][col0 + 8 * c] = top[c];
         }
         named_bar_sync(3, kSoftmaxThreads);
-        bool rescale = false;
         if (has_cols) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float m = fmaxf(top[c], sm.part[rh ^ 1][col0 + 8 * c]);
             float al = 1.f;
-            if (m > mr[c] + kLazyRaise) {
-              al = ex2(mr[c] - m);  // 0 while the maximum is -inf
-              mr[c] = m;
+            if (m > ref[c] + kRaiseTo) {
+              al = ex2(ref[c] - (m - kRaiseTo));  // 0 while nothing has been seen
+              ref[c] = m - kRaiseTo;
             }
             l_part[c] *= al;
-            rescale |= al != 1.f;
             if ((lane & 3) == 0 && rh == 0) sm.alpha[col0 + 8 * c] = al;
           }
         }
-        // O^T's columns lie across all four quadrants: each warp scales its lanes
-        if (softmax_any(rescale) && n > 0) {
+        if (n > 0) {
+          // O^T's columns lie across all four quadrants: each warp scales its lanes.
+          named_bar_sync(3, kSoftmaxThreads);  // alpha is written again behind two more barriers
           const int last = n - 1;  // its O^T must be done; this tile's waits for its P
           ok = wait_bar_warp(&sm.abort_flag, &sm.free_[last % n_bufs], static_cast<uint32_t>(last / n_bufs) & 1u, fw);
           if (!ok) atomicMin(&sm.abort_tile, n + 1);
@@ -734,19 +739,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
-          named_bar_sync(3, kSoftmaxThreads);  // alpha may be written again
         }
       }
       if (has_cols) {
-        // a masked z is -inf, and so is the maximum of a column that has seen nothing
-        const float sub[2] = {mr[0] == -INFINITY ? 0.f : mr[0], mr[1] == -INFINITY ? 0.f : mr[1]};
+        // a masked z is -inf, and so is the reference of a column that has seen nothing
+        const float sub[2] = {ref[0] == -INFINITY ? 0.f : ref[0], ref[1] == -INFINITY ? 0.f : ref[1]};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             // The denominator sums P before its rounding to f16 (operand type of
-            // the product): the LSE keeps float accuracy, and the output's
-            // share of that rounding is at most 2^-11.
+            // the product): the LSE keeps float accuracy.  Each row's weight in
+            // the output is off by at most 2^-11 of itself, or 2^-34 of the
+            // largest where that is more.
             const float p0 = ex2(z[4 * k + 2 * c] - sub[c]), p1 = ex2(z[4 * k + 2 * c + 1] - sub[c]);
             l_part[c] += p0 + p1;
             *reinterpret_cast<__half2*>(tile + kPOff + (2 * quad + c) * kPGroupBytes + (2 * rh + k) * 128 +
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         const int col = col0 + 8 * c;
         const float l = l_part[c] + sm.part[1][col];
         sm.alpha[col] = l == 0.f ? 0.f : 1.f / l;  // 0 when the column saw nothing
-        const float lse2 = l == 0.f ? -INFINITY : mr[c] + lg2(l);
+        const float lse2 = l == 0.f ? -INFINITY : ref[c] + lg2(l);
         if (ok && !direct)
           args.part_lse[(u.col0 + col) * args.parts + u.part] = lse2;
         else if (ok && args.lse != nullptr)

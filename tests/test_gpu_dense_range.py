@@ -1,0 +1,66 @@
+"""Dense decodes whose softmax weights span many binary orders: a first token far
+above the rows that the output is made of, against float64 relative to those
+rows."""
+import math
+
+import pytest
+import torch
+
+from dense_ref import LSE_TOL, ROW_BYTES, SCALE, attend64, random_pool, rows64, window_positions
+from gpu_helpers import lib
+from test_gpu_dense_decode import DEV, gen, lens_tensor, queries, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    return lib()
+
+
+def sink_case(g, fmt, lens, heads, bits, first):
+    """(pool, stride, tables, blocks, queries): row 0 of table entry `first[b]` has no
+    latent and a score `bits` binary orders above the others, whose scores
+    differ by a few hundredths: the output is those rows' alone."""
+    bt, spare, nb = tables(g, lens, extra_blocks=2)
+    pool, stride = random_pool(g, nb, fmt)
+    rows = pool.view(nb, 64, ROW_BYTES[fmt])
+    rope = slice(ROW_BYTES[fmt] - 64, ROW_BYTES[fmt])
+    rows[:, :, rope] = 0
+    for block in first(bt, spare):
+        rows[block, 0, :512 if fmt == 1 else 288] = 0
+        rows[block, 0, ROW_BYTES[fmt] - 64] = 0x50  # e4m3 8.0
+    qn, qr = queries(g, len(lens), 1, heads)
+    qn *= 2.0 ** -10
+    qr.zero_()
+    qr[..., 0] = torch.linspace(bits, bits + 0.9, heads, device=DEV) / (8.0 * SCALE * math.log2(math.e))
+    return pool, stride, bt, spare, nb, qn, qr
+
+
+def assert_tail(out, lse, qn, qr, rows):
+    """Against float64, relative to the rows that the output is made of.  Roundings
+    as in out_tolerance, but no f16 partial; the weight of a row below 2^-23 of
+    the largest is off by at most 2^-34 of that."""
+    ref, rl, a = attend64(qn, qr, rows)
+    v = rows[:, :512].abs().sum(0)
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -9) * a + 2.0 ** -34 * v + 1e-30
+    err = (out.double() - ref).abs()
+    assert (err <= tol).all(), f"{((err - tol) / (a + 1e-30)).max().item():.2e} of the weighted magnitude past it"
+    assert (lse.double() - rl).abs().max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("bits", [16, 20, 24, 30])
+def test_first_token_far_above_the_window(m, fmt, bits):
+    """One slice a request: the window's rows, 16 to 30 binary orders below a
+    first token whose latent is zero, keep their precision."""
+    g = gen(50 + bits)
+    lens = [600] * 170
+    pool, stride, bt, _, nb, qn, qr = sink_case(g, fmt, lens, 64, bits, lambda bt, _: [int(b) for b in bt[:, 0]])
+    assert m.mla_window_decode_workspace_size(170, 1, 64, bt.shape[1], 1, 300) == 0
+    lse = torch.empty((170, 1, 64), device=DEV)
+    out, _ = m.mla_window_decode(qn, qr, pool, stride, nb, bt, lens_tensor(lens), SCALE, 1, 300, fmt=fmt, lse=lse)
+    torch.cuda.synchronize()
+    pos = torch.tensor(window_positions(600, 1, 0, 1, 300, 640), device=DEV)
+    for b in (0, 50, 169):
+        assert_tail(out[b, 0], lse[b, 0], qn[b, 0], qr[b, 0], rows64(pool, fmt, bt[b], pos))
