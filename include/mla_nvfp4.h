@@ -508,7 +508,8 @@ mla_status_t mla_kv_norm_rope_append(const uint16_t* kv, int64_t kv_token_stride
  * Every row that a token of the call sees is read once per 64 (query token,
  * head) pairs of its request.  The weights of the rows in out are FP16 operands:
  * each is off by at most 2^-11 of itself, or by 2^-34 of the query's largest
- * weight in the same slice where that is more (rows 2^23 below it and further).
+ * weight in the same slice where that is more (rows 2^23 below it and further);
+ * the slices' partial outputs are float.
  *
  *   q_nope        device bf16 [batch, q_len, num_heads, 512]
  *   q_rope        device bf16 [batch, q_len, num_heads, 64], 16-byte aligned

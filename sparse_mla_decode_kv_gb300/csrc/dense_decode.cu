@@ -13,7 +13,8 @@
 // heads fill columns; where the rows are a shared prefix, so do the requests.
 //
 // Work split.  One CTA = 64 columns x a slice of their tiles; slices' partial
-// outputs (normalised, f16) and base-2 LSEs are joined by dense_merge_kernel.
+// outputs (normalised, float: behind a dominating row without a latent they can be
+// far below f16's range) and base-2 LSEs are joined by dense_merge_kernel.
 // Roles: one lane issues every tcgen05.mma; one copies each tile, which is
 // contiguous, with one bulk copy; 8 warps unpack a tile (8 rows x half the dims
 // each); 8 run its softmax (16 columns x 16 rows each); all write the output.
@@ -808,8 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
         const int64_t col = u.col0 + 16 * cg + j;
         if (direct)
           args.out[col * kLatent + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-        else  // a convex combination of cached values (|x| <= 6 x 448): f16 keeps 11 significant bits
-          args.part_o[(col * args.parts + u.part) * kLatent + dim] = __float2half_rn(x);
+        else
+          args.part_o[(col * args.parts + u.part) * kLatent + dim] = x;
       }
     }
   }
@@ -836,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
 // Coherent loads from L2: this grid may be resident before the partials are
 // written, which the read-only path does not allow.
 constexpr int kMergeChunk = 8;
-__global__ void __launch_bounds__(128) dense_merge_kernel(const __half* __restrict__ part_o,
+__global__ void __launch_bounds__(128) dense_merge_kernel(const float* __restrict__ part_o,
                                                           const float* __restrict__ part_lse, int parts,
                                                           uint16_t* __restrict__ out, float* __restrict__ lse) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -844,17 +845,17 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __half* __restri
   const int64_t col = blockIdx.x;
   const int t = threadIdx.x;
   const float* pl = part_lse + col * parts;
-  const uint2* src = reinterpret_cast<const uint2*>(part_o + col * parts * kLatent) + t;
+  const float4* src = reinterpret_cast<const float4*>(part_o + col * parts * kLatent) + t;
   float mx = -INFINITY, wsum = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < parts; s0 += kMergeChunk) {
     float ls[kMergeChunk];
-    uint2 v[kMergeChunk];
+    float4 v[kMergeChunk];
 #pragma unroll
     for (int i = 0; i < kMergeChunk; ++i) ls[i] = s0 + i < parts ? __ldcg(pl + s0 + i) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < kMergeChunk; ++i)
-      v[i] = ls[i] != -INFINITY ? __ldcg(src + static_cast<int64_t>(s0 + i) * (kLatent / 4)) : make_uint2(0, 0);
+      v[i] = ls[i] != -INFINITY ? __ldcg(src + static_cast<int64_t>(s0 + i) * (kLatent / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
     float cm = mx;
 #pragma unroll
     for (int i = 0; i < kMergeChunk; ++i) cm = ls[i] > cm || isnan(ls[i]) ? ls[i] : cm;
@@ -868,11 +869,10 @@ __global__ void __launch_bounds__(128) dense_merge_kernel(const __half* __restri
     for (int i = 0; i < kMergeChunk; ++i) {
       const float w = ex2(ls[i] - mx);
       wsum += w;
-      const __half2 a = *reinterpret_cast<const __half2*>(&v[i].x), b = *reinterpret_cast<const __half2*>(&v[i].y);
-      acc[0] += w * __low2float(a);
-      acc[1] += w * __high2float(a);
-      acc[2] += w * __low2float(b);
-      acc[3] += w * __high2float(b);
+      acc[0] += w * v[i].x;
+      acc[1] += w * v[i].y;
+      acc[2] += w * v[i].z;
+      acc[3] += w * v[i].w;
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
@@ -942,7 +942,7 @@ DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_row
   }
   const size_t parts = static_cast<size_t>(p.prefix_splits) + p.splits;
   if (parts > 1)
-    p.workspace = (static_cast<size_t>(columns) * parts * (kLatent * sizeof(__half) + sizeof(float)) + 255) / 256 * 256;
+    p.workspace = (static_cast<size_t>(columns) * parts * ((kLatent + 1) * sizeof(float)) + 255) / 256 * 256;
   return p;
 }
 
@@ -956,8 +956,8 @@ cudaError_t launch_dense_decode(int fmt, DenseArgs a, const DensePlan& plan, voi
   a.fault_word = fault_word_ptr();
   if (a.fault_word == nullptr) return cudaErrorInvalidDevicePointer;
   if (a.parts > 1) {
-    const size_t o_bytes = static_cast<size_t>(a.columns) * a.parts * kLatent * sizeof(__half);
-    a.part_o = static_cast<__half*>(workspace);
+    const size_t o_bytes = static_cast<size_t>(a.columns) * a.parts * kLatent * sizeof(float);
+    a.part_o = static_cast<float*>(workspace);
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
   }
   const void* kernel = fmt == 0 ? reinterpret_cast<const void*>(dense_decode_kernel<0>)
@@ -970,7 +970,7 @@ cudaError_t launch_dense_decode(int fmt, DenseArgs a, const DensePlan& plan, voi
   void* params[] = {&a};
   e = launch_dependent(kernel, static_cast<unsigned>(units), kThreads, kSmemBytes, params, stream);
   if (e != cudaSuccess || a.parts == 1) return e;
-  const __half* po = a.part_o;
+  const float* po = a.part_o;
   const float* pl = a.part_lse;
   void* merge[] = {&po, &pl, &a.parts, &a.out, &a.lse};
   return launch_dependent(reinterpret_cast<const void*>(dense_merge_kernel), static_cast<unsigned>(a.columns), 128, 0,

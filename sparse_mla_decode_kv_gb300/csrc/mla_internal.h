@@ -6,7 +6,6 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace mla {
@@ -122,7 +121,7 @@ struct DenseArgs {
   // set by the launch from the plan
   int groups_per_req, splits, prefix_groups, prefix_splits, parts;
   int64_t columns;
-  __half* part_o;
+  float* part_o;
   float* part_lse;
   unsigned int* fault_word;
 };

@@ -64,3 +64,59 @@ def test_first_token_far_above_the_window(m, fmt, bits):
     pos = torch.tensor(window_positions(600, 1, 0, 1, 300, 640), device=DEV)
     for b in (0, 50, 169):
         assert_tail(out[b, 0], lse[b, 0], qn[b, 0], qr[b, 0], rows64(pool, fmt, bt[b], pos))
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("bits", [16, 24])
+def test_first_token_far_above_in_one_of_several_slices(m, fmt, bits):
+    """The slice with that token keeps its other rows' part of the output, small
+    as it is; so does a prefix that holds it."""
+    g = gen(60 + bits)
+    lens = [5000, 4000]
+    pool, stride, bt, _, nb, qn, qr = sink_case(g, fmt, lens, 16, bits, lambda bt, _: [int(b) for b in bt[:, 0]])
+    assert m.mla_window_decode_workspace_size(2, 1, 16, bt.shape[1], 0, 5000) > 0
+    lse = torch.empty((2, 1, 16), device=DEV)
+    out, _ = m.mla_window_decode(qn, qr, pool, stride, nb, bt, lens_tensor(lens), SCALE, 0, 5000, fmt=fmt, lse=lse)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        rows = rows64(pool, fmt, bt[b], torch.arange(n, device=DEV))
+        assert_tail(out[b, 0], lse[b, 0], qn[b, 0], qr[b, 0], rows)
+
+    lens = [40, 0, 7]
+    pool, stride, bt, pt, nb, qn, qr = sink_case(g, fmt, lens, 32, bits, lambda _, spare: [int(spare[0])])
+    lse = torch.empty((3, 1, 32), device=DEV)
+    out, _ = m.mla_prefix_decode(qn, qr, pool, stride, nb, pt, 100, bt, lens_tensor(lens), SCALE, 40, fmt=fmt, lse=lse)
+    torch.cuda.synchronize()
+    shared = rows64(pool, fmt, pt, torch.arange(100, device=DEV))
+    for b, n in enumerate(lens):
+        rows = torch.cat([shared, rows64(pool, fmt, bt[b], torch.arange(n, device=DEV))])
+        assert_tail(out[b, 0], lse[b, 0], qn[b, 0], qr[b, 0], rows)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_wide_scores(m, fmt):
+    """Scores with a deviation of 20 binary orders: maxima are raised in many tiles, of one column or another."""
+    g = gen(70)
+    lens = [1500, 700, 1501]
+    bt, _, nb = tables(g, lens)
+    pool, stride = random_pool(g, nb, fmt)
+    qn, qr = queries(g, 3, 2, 64)
+    qn, qr = qn * 8, qr * 8
+    lse = torch.empty((3, 2, 64), device=DEV)
+    out, _ = m.mla_window_decode(qn, qr, pool, stride, nb, bt, lens_tensor(lens), SCALE, 4, 1400, fmt=fmt, lse=lse)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        for i in range(2):
+            pos = torch.tensor(window_positions(n, 2, i, 4, 1400, bt.shape[1] * 64), device=DEV)
+            rows = rows64(pool, fmt, bt[b], pos)
+            ref, rl, a = attend64(qn[b, i], qr[b, i], rows)
+            # a score's float accumulation: 576 x 2^-24 x the sum of |q k| scale, which
+            # moves the LSE by at most itself and the output by twice that share of A;
+            # weights 2^23 below the largest are off by at most 2^-34 of it, which counts
+            # where the largest's value is 0
+            v = rows[:, :512].abs().sum(0)
+            q = torch.cat([qn[b, i], qr[b, i]], -1).double().abs()
+            d = 576 * 2.0 ** -24 * (q @ rows.abs().t()).max().item() * SCALE
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * d) * a + 2.0 ** -34 * v
+            assert ((out[b, i].double() - ref).abs() <= tol).all()
+            assert (lse[b, i].double() - rl).abs().max() <= d + 2.0 ** -20
