@@ -903,10 +903,14 @@ cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, 
 
 // How the rows are split: modelled time of one CTA = its tiles + kStartTiles
 // (start-up, query load and output, in tiles), of the call = full waves of
-// the prefix's CTAs, with the own rows' CTAs (no longer than the prefix's) in
-// the SMs that the last of those waves leaves idle and in waves of their own
-// after it, + the joining of the partials (about four tiles, and one for every
-// 6).  In eighths of a tile; the fewest partials among equals.
+// the prefix's CTAs, with the own rows' CTAs in the SMs that the last of those
+// waves leaves idle and in waves of their own after it, + the joining of the
+// partials (about four tiles, and one for every 6).  In eighths of a tile; the
+// fewest partials among equals.  The own rows' slices are as long as the prefix's,
+// or, where that makes more of them than a call without a prefix has, the number
+// of that call if it is better: a prefix of one tile must not cut long contexts
+// into single tiles (32 requests x 16 heads, 140,000 own rows behind a prefix of
+// 500: 274 slices, now 19).
 DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_rows, int prefix_len) {
   constexpr int64_t kStartTiles = 8;
   DensePlan p{1, 1, 0, 0, 0};
@@ -921,22 +925,31 @@ DensePlan plan_dense_decode(int batch, int q_len, int num_heads, int64_t own_row
   p.prefix_groups = static_cast<int>(pre_groups);
   const int64_t tiles = pre_tiles > 0 ? pre_tiles : own_tiles;
   const int64_t groups = pre_tiles > 0 ? pre_groups : own_groups;
+  const int64_t alone = pre_tiles > 0 ? plan_dense_decode(batch, q_len, num_heads, own_rows, 0).splits : 0;
   int64_t best = -1;
   for (int64_t n = 1; n <= tiles && n <= sms; ++n) {
     const int64_t slice = (tiles + n - 1) / n;
     const int64_t waves = (groups * n + sms - 1) / sms;
-    int64_t cost = 8 * waves * (slice + kStartTiles), s = 0;
-    if (pre_tiles > 0) {
-      const int64_t own_slice = own_tiles < slice ? own_tiles : slice;
-      s = (own_tiles + own_slice - 1) / own_slice;
-      const int64_t fit = (waves * sms - groups * n) * ((slice + kStartTiles) / (own_slice + kStartTiles));
-      if (own_groups * s > fit) cost += 8 * ((own_groups * s - fit + sms - 1) / sms) * (own_slice + kStartTiles);
-    }
-    if (n + s > 1) cost += 32 + 4 * (n + s) / 3;
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.prefix_splits = static_cast<int>(pre_tiles > 0 ? n : 0);
-      p.splits = static_cast<int>(pre_tiles > 0 ? s : n);
+    auto consider = [&](int64_t s) {  // n slices of the prefix and s of the own rows (0: n of the own rows)
+      int64_t cost = 8 * waves * (slice + kStartTiles);
+      if (s > 0) {
+        const int64_t own_slice = (own_tiles + s - 1) / s;
+        const int64_t fit = (waves * sms - groups * n) * ((slice + kStartTiles) / (own_slice + kStartTiles));
+        if (own_groups * s > fit) cost += 8 * ((own_groups * s - fit + sms - 1) / sms) * (own_slice + kStartTiles);
+      }
+      if (n + s > 1) cost += 32 + 4 * (n + s) / 3;
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.prefix_splits = static_cast<int>(s > 0 ? n : 0);
+        p.splits = static_cast<int>(s > 0 ? s : n);
+      }
+    };
+    if (pre_tiles == 0) {
+      consider(0);
+    } else {
+      const int64_t match = own_tiles > slice ? (own_tiles + slice - 1) / slice : 1;
+      if (match <= sms) consider(match);
+      if (match > alone) consider(alone);
     }
     if (groups * n > 4 * sms) break;  // every SM has several CTAs already
   }

@@ -8,7 +8,7 @@ import torch
 
 from dense_ref import LSE_TOL, ROW_BYTES, SCALE, attend64, random_pool, rows64, window_positions
 from gpu_helpers import lib
-from test_gpu_dense_decode import DEV, gen, lens_tensor, queries, tables
+from test_gpu_dense_decode import DEV, gen, lens_tensor, prefix_case, queries, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,11 @@ def test_wide_scores(m, fmt):
             tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * d) * a + 2.0 ** -34 * v
             assert ((out[b, i].double() - ref).abs() <= tol).all()
             assert (lse[b, i].double() - rl).abs().max() <= d + 2.0 ** -20
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("prefix,lens,q_len,heads", [(1, [3000, 5, 2500], 1, 16), (33, [9000], 2, 32),
+                                                     (500, [2000] * 40, 1, 64)])
+def test_prefix_much_shorter_than_the_own_rows(m, fmt, prefix, lens, q_len, heads):
+    """The own rows have fewer slices than prefix-sized ones would be."""
+    prefix_case(m, 80 + prefix, fmt, prefix, lens, q_len, heads)
