@@ -451,7 +451,8 @@ mla_status_t mla_block_table_extend(const int32_t* context_lens, const int32_t* 
  *     in, out     device bf16, 16-byte aligned; head h of token t starts at
  *                 t * token stride + h * head stride (elements, multiples of
  *                 8); out may be in with the same strides, else no element
- *                 of one may be in the other
+ *                 of one may be in the other; no two heads of out may share
+ *                 an element (checked), nor the outputs of q and k
  *     weight      device bf16 [head_dim], 16-byte aligned, or NULL: no norm
  *   head_dim      64..256, a multiple of 8 (wider: MLA_ERR_UNSUPPORTED)
  *   rope_offset   0..head_dim - 64, a multiple of 8

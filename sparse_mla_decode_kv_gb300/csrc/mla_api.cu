@@ -121,6 +121,20 @@ mla_status_t run_dense(int fmt, const DenseArgs& a, const DensePlan& plan, void*
   return cuda_status(launch_dense_decode(fmt, a, plan, workspace, stream));
 }
 
+// Whether two of n x m rows of `dim` elements, row (i, j) at i * s + j * t with
+// s, t >= dim, share an element: i s - j t is within dim of 0 for an i in 1..n-1
+// and a j in 1..m-1.
+bool rows_overlap(int64_t n, int64_t s, int64_t m, int64_t t, int64_t dim) {
+  using Wide = __int128;  // strides are the caller's: products may pass 64 bits
+  if (n < 2 || m < 2) return false;
+  if (static_cast<Wide>(m - 1) * t + dim <= s || static_cast<Wide>(n - 1) * s + dim <= t) return false;  // nested
+  if (m > n) return rows_overlap(m, t, n, s, dim);
+  for (int64_t j = 1; j < m; ++j) {
+    const Wide at = static_cast<Wide>(j) * t, i = at / s;  // the nearest rows of the other kind: i and i + 1
+    if ((i >= 1 && i < n && at - i * s < dim) || (i + 1 < n && (i + 1) * s - at < dim)) return true;
+  }
+  return false;
+}
 mla_status_t check_heads(const mla_heads_t* h, int64_t n_tokens, int head_dim) {
   if (h->heads < 0) return MLA_ERR_INVALID_ARG;
   if (h->heads == 0 || n_tokens == 0) return MLA_OK;
@@ -128,9 +142,10 @@ mla_status_t check_heads(const mla_heads_t* h, int64_t n_tokens, int head_dim) {
   if (h->weight && !aligned(h->weight, 16)) return MLA_ERR_INVALID_ARG;
   if (h->in_token_stride % 8 || h->in_head_stride % 8 || h->out_token_stride % 8 || h->out_head_stride % 8)
     return MLA_ERR_INVALID_ARG;
-  // two rows of the output must not be one
+  // no two rows of the output may share an element
   if (n_tokens > 1 && h->out_token_stride < head_dim) return MLA_ERR_INVALID_ARG;
   if (h->heads > 1 && h->out_head_stride < head_dim) return MLA_ERR_INVALID_ARG;
+  if (rows_overlap(n_tokens, h->out_token_stride, h->heads, h->out_head_stride, head_dim)) return MLA_ERR_INVALID_ARG;
   if (h->in == h->out && ((n_tokens > 1 && h->in_token_stride != h->out_token_stride) ||
                           (h->heads > 1 && h->in_head_stride != h->out_head_stride)))
     return MLA_ERR_INVALID_ARG;
