@@ -318,7 +318,7 @@ __device__ __forceinline__ Unit find_unit(const DenseArgs& a) {
     u.table = a.block_table + static_cast<int64_t>(b) * a.max_blocks;
     u.table_len = a.max_blocks;
     u.masked = true;
-    const int ctx = min(max(__ldg(a.ctx_lens + b), 0), a.max_context);
+    const int ctx = min(max(a.ctx_lens[b], 0), a.max_context);
     u.me0 = ctx - a.q_len;
     const int me_lo = u.me0 + u.tok_col0 / a.num_heads;
     const int me_hi = u.me0 + (u.tok_col0 + u.ncols - 1) / a.num_heads;
@@ -342,11 +342,14 @@ __device__ __forceinline__ int tile_pos(const Unit& u, int t) {
   return (t < u.n_sink_tiles ? t : u.w_tile + (t - u.n_sink_tiles)) * kRows;
 }
 // Physical block of tile t as the table has it (it may lie outside the pool),
-// -1 past the slice or the table.
+// -1 past the slice or the table.  Lengths and tables are plain loads, which the
+// wait for the kernel in front orders behind its writes: this grid may be resident
+// before they are made, and the read-only path does not allow that.  (From L2, as
+// the queries, they cost 2 %: 121 -> 123.5 us for 128 requests x 64 heads.)
 __device__ __forceinline__ int tile_id(const Unit& u, int t) {
   if (t >= u.end) return -1;
   const int blk = tile_pos(u, t) / kBlock;
-  return blk < u.table_len ? __ldg(u.table + blk) : -1;
+  return blk < u.table_len ? u.table[blk] : -1;
 }
 
 template <int FMT>
@@ -442,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
     // 8 columns x 32 dims at a time (64-byte pieces of 8 rows in, conflict-free
     // 16-byte stores out); every load is issued before the first is used.  A
     // column whose query holds an infinity or NaN enters as zeros with a NaN
-    // scale: its results are NaN, its neighbours' are not.
-    // Coherent loads, as an earlier call's output may be the query.
+    // scale: its results are NaN, its neighbours' are not.  Coherent loads, as an
+    // earlier call's output may be the query.
     constexpr int kPieces = kDimGroups / 4;               // of 32 dims
     constexpr int kPer = (kCols / 8) * kPieces / kWarps;  // 9
     const int n_tasks = (u.ncols / 8) * kPieces;
