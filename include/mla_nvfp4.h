@@ -450,9 +450,10 @@ mla_status_t mla_block_table_extend(const int32_t* context_lens, const int32_t* 
  *   q, k          head sets on the host, either may be NULL (or have 0 heads)
  *     in, out     device bf16, 16-byte aligned; head h of token t starts at
  *                 t * token stride + h * head stride (elements, multiples of
- *                 8); out may be in with the same strides, else no element
- *                 of one may be in the other; no two heads of out may share
- *                 an element (checked), nor the outputs of q and k
+ *                 8; that of an axis with one entry is not used); out may
+ *                 be in with the same strides, else no element of one may be
+ *                 in the other; no two heads of out may share an element
+ *                 (checked), nor the outputs of q and k
  *     weight      device bf16 [head_dim], 16-byte aligned, or NULL: no norm
  *   head_dim      64..256, a multiple of 8 (wider: MLA_ERR_UNSUPPORTED)
  *   rope_offset   0..head_dim - 64, a multiple of 8
@@ -482,7 +483,7 @@ mla_status_t mla_qk_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_
  *
  *   kv            device bf16 [n_tokens, 512 latent + 64 key], 16-byte
  *                 aligned, rows kv_token_stride elements apart (a multiple
- *                 of 8)
+ *                 of 8; not used with one token)
  *   latent_weight device bf16 [512], 16-byte aligned
  *   slot_mapping, kv_pool, num_blocks, block_size, kv_block_stride, fmt
  *                 as for mla_kv_quantize_append

@@ -140,8 +140,9 @@ mla_status_t check_heads(const mla_heads_t* h, int64_t n_tokens, int head_dim) {
   if (h->heads == 0 || n_tokens == 0) return MLA_OK;
   if (!h->in || !h->out || !aligned(h->in, 16) || !aligned(h->out, 16)) return MLA_ERR_INVALID_ARG;
   if (h->weight && !aligned(h->weight, 16)) return MLA_ERR_INVALID_ARG;
-  if (h->in_token_stride % 8 || h->in_head_stride % 8 || h->out_token_stride % 8 || h->out_head_stride % 8)
-    return MLA_ERR_INVALID_ARG;
+  // the stride of an axis of one entry is not used
+  if (n_tokens > 1 && (h->in_token_stride % 8 || h->out_token_stride % 8)) return MLA_ERR_INVALID_ARG;
+  if (h->heads > 1 && (h->in_head_stride % 8 || h->out_head_stride % 8)) return MLA_ERR_INVALID_ARG;
   // no two rows of the output may share an element
   if (n_tokens > 1 && h->out_token_stride < head_dim) return MLA_ERR_INVALID_ARG;
   if (h->heads > 1 && h->out_head_stride < head_dim) return MLA_ERR_INVALID_ARG;
@@ -627,7 +628,7 @@ mla_status_t mla_kv_norm_rope_append(const uint16_t* kv, int64_t kv_token_stride
   if (s != MLA_OK || n_tokens == 0) return s;
   if (!kv || !latent_weight || !slot_mapping || !kv_pool) return MLA_ERR_INVALID_ARG;
   if (!aligned(kv, 16) || !aligned(latent_weight, 16) || !aligned(slot_mapping, 8) || !aligned(kv_pool, 16) ||
-      kv_token_stride % 8 != 0)
+      (n_tokens > 1 && kv_token_stride % 8 != 0))
     return MLA_ERR_INVALID_ARG;
   NormRopeArgs a{};
   a.set[0] = head_set(q);

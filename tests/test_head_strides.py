@@ -66,3 +66,31 @@ def test_other_strides_are_taken(m, n, heads, token, head):
     expect = torch.full_like(buf, 7.0)
     expect.as_strided((n, heads, 64), (token, head, 1)).copy_(want)
     assert torch.equal(buf, expect)
+
+
+@pytest.mark.gpu
+def test_strides_of_one_token_or_head_are_not_used(m):
+    """Views whose axis of one entry has a stride that is no multiple of 8."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def bf16(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    inv = torch.full((32,), 0.5, dtype=torch.float64, device="cuda")
+    pos = torch.tensor([1000], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([5], dtype=torch.int64, device="cuda")
+    w, wq = bf16(512), bf16(128)
+    kv, q = bf16(1, 576), bf16(1, 3, 128)
+    got = []
+    for kv_in, q_in in ((kv, q), (kv.as_strided((1, 576), (579, 1)), q.as_strided((1, 3, 128), (13, 128, 1)))):
+        pool = torch.zeros((1, 64, 352), dtype=torch.uint8, device="cuda")
+        out = m.mla_kv_norm_rope_append(kv_in, w, pos, inv, slots, pool, 1, 64, 64 * 352, q=q_in, q_weight=wq,
+                                        q_out=torch.empty_like(q).as_strided((1, 3, 128), (3, 128, 1)))
+        got.append((pool, out.clone()))
+    k, pos = bf16(9, 1, 128), torch.arange(9, dtype=torch.int32, device="cuda")
+    a, _ = m.mla_qk_norm_rope(k, None, pos, inv, q_weight=wq)
+    b, _ = m.mla_qk_norm_rope(k.as_strided((9, 1, 128), (128, 3, 1)), None, pos, inv, q_weight=wq)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][0], got[1][0]) and got[0][0].any()
+    assert torch.equal(got[0][1], got[1][1]) and torch.equal(a, b)
