@@ -457,7 +457,22 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(v, name) -> None:
+    """Refuses what a C int would keep the low 32 bits of."""
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise ValueError(f"{name} {v} does not fit 32 bits")
+
+
+def _length(v, name) -> int:
+    """A length cut to the longest that a context can have."""
+    if v < 0:
+        _c_int(v, name)
+    return min(v, _INT_MAX)
+
+
 def _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt) -> None:
+    _c_int(block_size, "block_size")
+    _c_int(fmt, "fmt")
     if num_blocks > 0 and kv_pool.numel() * kv_pool.element_size() < (num_blocks - 1) * kv_block_stride + \
             block_size * (352 if fmt == MLA_KV_NVFP4 else 576):
         raise ValueError("kv_pool does not reach the last row of block num_blocks - 1")
@@ -482,6 +497,7 @@ def mla_block_table_extend(context_lens, new_lens, block_table, free_blocks, fre
     if block_table.dim() != 2 or block_table.shape[0] != batch or new_lens.numel() != batch or \
             free_state.numel() != 3:
         raise ValueError("new_lens [B], block_table [B, W] and free_state [3] must fit context_lens [B]")
+    _c_int(block_size, "block_size")
     slot_mapping = _take(slot_mapping, (num_slots,), torch.int64, "slot_mapping", free_state, stream)
     positions = _take(positions, (num_slots,), torch.int32, "positions", context_lens, stream)
     query_start = _take(query_start, (batch + 1,), torch.int32, "query_start", context_lens, stream)
@@ -524,7 +540,8 @@ def _heads(x, weight, out, name, stream):
                   None if weight is None else weight.data_ptr()), out
 
 
-def _angles(positions, inv_freq, n):
+def _angles(positions, inv_freq, n, rope_offset):
+    _c_int(rope_offset, "rope_offset")
     if _contig(positions, torch.int32, "positions").numel() != n:
         raise ValueError(f"positions must have one entry for each of {n} tokens")
     if _contig(inv_freq, torch.float64, "inv_freq").numel() != 32:
@@ -540,7 +557,7 @@ def mla_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     device = _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     hq, q_out = _heads(q, q_weight, q_out, "q", stream)
     n, _, dim = q.shape
-    _angles(positions, inv_freq, n)
+    _angles(positions, inv_freq, n, rope_offset)
     hk = None
     if k is not None:
         hk, k_out = _heads(k, k_weight, k_out, "k", stream)
@@ -570,7 +587,7 @@ def mla_kv_norm_rope_append(kv, latent_weight, positions, inv_freq, slot_mapping
         raise ValueError("latent_weight must have 512 values")
     if _contig(slot_mapping, torch.int64, "slot_mapping").numel() != n:
         raise ValueError(f"slot_mapping must have one entry for each of {n} tokens")
-    _angles(positions, inv_freq, n)
+    _angles(positions, inv_freq, n, rope_offset)
     _check_pool(kv_pool, num_blocks, block_size, kv_block_stride, fmt)
     hq = None
     if q is not None:
@@ -608,6 +625,7 @@ def _dense_tensors(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_t
 
 def mla_window_decode_workspace_size(batch: int, q_len: int, num_heads: int, max_blocks_per_req: int, sinks: int,
                                      window: int) -> int:
+    sinks, window = _length(sinks, "sinks"), _length(window, "window")
     return int(load().mla_window_decode_workspace_size(batch, q_len, num_heads, max_blocks_per_req, sinks, window))
 
 
@@ -620,7 +638,7 @@ def mla_window_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, bloc
     q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
-    sinks, window = min(sinks, _INT_MAX), min(window, _INT_MAX)  # no context is longer
+    sinks, window = _length(sinks, "sinks"), _length(window, "window")
     if workspace is None:
         need = mla_window_decode_workspace_size(batch, q_len, heads, block_table.shape[1], sinks, window)
         workspace = _new(kv_pool, (need,), torch.uint8, stream) if need > 0 else None
@@ -635,6 +653,8 @@ def mla_window_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, bloc
 
 def mla_prefix_decode_workspace_size(batch: int, q_len: int, num_heads: int, prefix_len: int,
                                      max_blocks_per_req: int, max_context_len: int) -> int:
+    max_context_len = _length(max_context_len, "max_context_len")
+    _c_int(prefix_len, "prefix_len")
     return int(load().mla_prefix_decode_workspace_size(batch, q_len, num_heads, prefix_len, max_blocks_per_req,
                                                        max_context_len))
 
@@ -649,9 +669,8 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
     q_nope, q_rope, batch, q_len, heads, out, device = _dense_tensors(
         q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, block_table, context_lens, fmt, block_size, out, lse,
         workspace, stream)
-    if prefix_len > _INT_MAX:
-        raise ValueError("prefix_len is a 32-bit length")
-    max_context_len = min(max_context_len, _INT_MAX)
+    max_context_len = _length(max_context_len, "max_context_len")
+    _c_int(prefix_len, "prefix_len")
     if prefix_len > 0:
         _here(out, prefix_table)
         if _contig(prefix_table, torch.int32, "prefix_table").numel() * block_size < prefix_len:
