@@ -444,8 +444,9 @@ mla_status_t mla_block_table_extend(const int32_t* context_lens, const int32_t* 
  *   (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin)
  *
  * where pair i is values 2i and 2i + 1 (interleaved nonzero) or i and i + 32.
- * Float32 arithmetic, one rounding to bf16 at the end; the angle is kept as a
- * 64-bit fraction of a turn, exact for any 32-bit position.
+ * Float32 arithmetic, one rounding to bf16 at the end.  The angle is kept as a
+ * 64-bit fraction of a turn: for inv_freq up to 1 it is within 2^-31 +
+ * |position| x 2^-55 of a turn.
  *
  *   q, k          head sets on the host, either may be NULL (or have 0 heads)
  *     in, out     device bf16, 16-byte aligned; head h of token t starts at

@@ -23,18 +23,19 @@
 // MN-major A operand of O^T (M = 128 dims).  P lies in the tile's rope part,
 // which only S reads.
 //
-// What bounds it.  No pipe is full: the issuing lane never waits, but a tile
-// costs it ~1,700 cycles, 820 of them for the 36 MMAs of S (~23 each, which is
-// also what their operands take from shared memory), 175 for the 8 of O^T (which
-// run ~48 each), the rest barriers, commits and the loop; the softmax's serial
-// part is as long, so halving either alone changes nothing.  S of the next tile
-// is issued before O^T of this one.  32 rows a tile and not 64 or 128, so that
-// three unpacked tiles (37 KB each) fit beside a 72 KB query of 64 columns:
-// pieces of 64-row tiles took 204 us where this takes 118 (128 requests x 64
-// heads, window 4,096), 64-row tiles beside 16 columns 68 to 81 us where this
-// takes 64 (32 requests, window 8,192).  Slower as well: S two tiles ahead, an
-// issuing lane for each product, two softmax sets on tiles in turn, and S of the
-// next tile loaded while P is computed -- each delays O^T, which frees the tile.
+// What bounds it.  The issuing lane: a tile takes it ~1,640 cycles, ~900 for the
+// 36 MMAs of S (25 each, about what their operands take from shared memory), ~330
+// for the 8 of O^T (41 each), ~270 for the two polls, which find what they ask for
+// at the first or second try, ~150 for the two commits.  The tensor pipe is then
+// active in half of the cycles.  The softmax's serial part is as long, so halving
+// either alone changes nothing.  S of the next tile is issued before O^T of this
+// one.  32 rows a tile and not 64 or 128, so that three unpacked tiles (37 KB each)
+// fit beside a 72 KB query of 64 columns: pieces of 64-row tiles took 204 us where
+// this took 118 (128 requests x 64 heads, window 4,096; 121 since P keeps far rows'
+// weights), 64-row tiles beside 16 columns 68 to 81 us where this took 64 (32
+// requests, window 8,192).  Slower as well: S two tiles ahead, an issuing lane for
+// each product, two softmax sets on tiles in turn, and S of the next tile loaded
+// while P is computed -- each delays O^T, which frees the tile.
 //
 // Every wait is bounded; one that runs out sets the library's fault bit and
 // the CTA leaves after its copies and MMAs in flight have drained.
@@ -196,7 +197,7 @@ __device__ __noinline__ bool wait_bar_slow(int* abort_flag, uint64_t* bar, uint3
 __device__ __forceinline__ bool wait_bar(int* abort_flag, uint64_t* bar, uint32_t parity, unsigned int* fw) {
   return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_bar_slow(abort_flag, bar, parity, fw);
 }
-// The same for a whole warp: one lane polls.
+// The same for a whole warp: every lane polls, and all go on or none.
 __device__ __forceinline__ bool wait_bar_warp(int* abort_flag, uint64_t* bar, uint32_t parity, unsigned int* fw) {
   bool ok = true;
   if (!mbar_try_wait(bar, parity)) ok = wait_bar(abort_flag, bar, parity, fw);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // One lane runs the whole role with a tile's MMAs unrolled: they then issue
-    // at the tensor core's own rate (24 cycles at M = 64, N = 32; 40-48 at M =
+    // at the tensor core's own rate (25 cycles at M = 64, N = 32; 41-48 at M =
     // 128).  A warp-wide loop with an election per piece took twice that, and
     // rolled loops, whose operand registers wait for the previous MMA to
     // start, four times.

@@ -9,8 +9,10 @@
 // Angles.  position * inv_freq in float loses the angle of far positions
 // (2^20 x 2^-24 = 0.06 rad), and FP64 is slow here.  A turn fraction is kept
 // instead: inv_freq / 2 pi as a 64-bit fixed-point fraction of a turn, times
-// the position modulo 2^64 -- exact integer arithmetic -- whose upper 32 bits
-// are the phase to 2^-32 of a turn.  sincospi then sees an argument in [-1, 1].
+// the position modulo 2^64 in exact integer arithmetic, of which the upper 32 bits
+// are used.  The fraction comes from a double product, so for inv_freq up to 1 the
+// phase is within 2^-31 + |position| x 2^-55 of a turn (2^-24 at the ends of 32
+// bits).  sincospi then sees an argument in [-1/4, 1/4].
 //
 // Latent rows.  The normed latent and the rotated key are rounded to bf16 and
 // then quantised exactly as the quantize-on-write kernel quantises bf16 rows:
@@ -57,7 +59,7 @@ __device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__fl
 
 // sin and cos of position x the pair's frequency (a 64-bit fraction of a turn).
 // The nearest quarter turn is split off as an integer, so that the float holds
-// an eighth of a turn at most (its rounding is 2^-27 of a turn, not 2^-25).
+// an eighth of a turn at most (half a step of it is 2^-28 of a turn, not 2^-26).
 __device__ __forceinline__ void angle(uint64_t turn, int position, float* s, float* c) {
   const uint64_t phase = turn * static_cast<uint64_t>(static_cast<int64_t>(position));
   const uint32_t hi = static_cast<uint32_t>(phase >> 32);
