@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           top[c] = fmaxf(top[c], fmaxf(fmaxf(z[2 * c], z[2 * c + 1]), fmaxf(z[4 + 2 * c], z[4 + 2 * c + 1])));
-        need = isnan(nan_sum) || top[0] > ref[0] + kRaiseAt || top[1] > ref[1] + kRaiseAt;
+        // differences, as P's exponent is one: a sum would be rounded to far scores' step
+        need = isnan(nan_sum) || top[0] - ref[0] > kRaiseAt || top[1] - ref[1] > kRaiseAt;
       }
       if (!ok) atomicMin(&sm.abort_tile, n);
       // every softmax thread takes the same branch at every barrier: a failed
@@ -716,9 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const DenseAr
           for (int c = 0; c < 2; ++c) {
             const float m = fmaxf(top[c], sm.part[rh ^ 1][col0 + 8 * c]);
             float al = 1.f;
-            if (m > ref[c] + kRaiseTo) {
-              al = ex2(ref[c] - (m - kRaiseTo));  // 0 while nothing has been seen
-              ref[c] = m - kRaiseTo;
+            if (m - ref[c] > kRaiseTo) {
+              float to = m - kRaiseTo;
+              to = m - to > kRaiseAt ? m : to;  // at 2^27 the step is 16, which f16 does not hold
+              al = ex2(ref[c] - to);            // 0 while nothing has been seen
+              ref[c] = to;
             }
             l_part[c] *= al;
             if ((lane & 3) == 0 && rh == 0) sm.alpha[col0 + 8 * c] = al;

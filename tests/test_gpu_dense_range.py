@@ -128,3 +128,41 @@ def test_wide_scores(m, fmt):
 def test_prefix_much_shorter_than_the_own_rows(m, fmt, prefix, lens, q_len, heads):
     """The own rows have fewer slices than prefix-sized ones would be."""
     prefix_case(m, 80 + prefix, fmt, prefix, lens, q_len, heads)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("step", [0.0, 16.0])
+@pytest.mark.parametrize("level", [2.0 ** 18, 1.5 * 2.0 ** 19, 2.0 ** 25, 2.0 ** 26, 1.25 * 2.0 ** 27, 2.0 ** 28])
+def test_scores_whose_steps_are_coarse(m, fmt, step, level):
+    """Scores of 2^18 to 2^28 (base 2), whose float steps reach 32: the last rows stand
+    `step` above the others, and the output is a mean of rows, not an infinity."""
+    g = gen(100)
+    n = 200
+    bt, _, nb = tables(g, [n])
+    pool, stride = random_pool(g, nb, fmt)
+    rows, rope = pool.view(nb, 64, ROW_BYTES[fmt]), ROW_BYTES[fmt] - 64
+    rows[:, :, rope:] = 0
+    rows[:, :, rope] = 0x38  # e4m3 1.0
+    rows[bt[0, 2].long(), :, rope + 1] = 0x38
+    rows[bt[0, 3].long(), :, rope + 1] = 0x38
+    qn, qr = queries(g, 1, 1, 16)
+    qn.zero_()
+    qr.zero_()
+    qr[..., 0], qr[..., 1] = level, step
+    scale = math.log(2.0)  # a score is then q . k in base 2, but for the float of the two factors
+    lse = torch.empty((1, 1, 16), device=DEV)
+    out, _ = m.mla_window_decode(qn, qr, pool, stride, nb, bt, lens_tensor([n]), scale, 0, n, fmt=fmt, lse=lse)
+    torch.cuda.synchronize()
+    v = rows64(pool, fmt, bt[0], torch.arange(n, device=DEV))[:, :512]
+    got, h = out[0, 0].double(), 2.0 ** -24 * level
+    # between the rows' least and largest values, whatever the steps make of the differences
+    assert (got <= v.amax(0) * (1 + 2.0 ** -8) + 1e-6).all() and (got >= v.amin(0) * (1 + 2.0 ** -8) - 1e-6).all()
+    if step == 0.0:
+        # equal scores: P is the same power of two for every row of a slice.  Slices are
+        # joined by float LSEs of this size, of which half a step is h: a slice's weight is
+        # off by a factor of up to 2^h, and so is the sum it is divided by.
+        tol = 2.0 ** -8 * v.mean(0).abs() + (2.0 ** (2 * h) - 1 + 2.0 ** -16) * v.abs().mean(0)
+        assert ((got - v.mean(0)).abs() <= tol).all()
+    # eight float roundings (the scale's factors and product, the score, the sum with log2 of the
+    # denominator, ln 2 and its product), and a denominator of at most 200 x 2^16
+    assert ((lse.double() / math.log(2.0) - level).abs() <= 8 * 2.0 ** -24 * level + 24).all()
