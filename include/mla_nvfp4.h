@@ -561,6 +561,79 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
                                int max_context_len, float softmax_scale, mla_kv_format_t fmt, uint16_t* out,
                                float* lse, void* workspace, size_t workspace_bytes, mla_stream_t stream);
 
+/*
+ * The residual's addition, the norm behind it, and its output in 8 bits.  For
+ * every row of dim values:
+ *
+ *   h = x + residual                    (h = x without one)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *   scales[g] = max |y_i| / 448  over group g,   codes[i] = e4m3(y_i / scales[g])
+ *
+ * in float32, e4m3 rounded to nearest even.  h is rounded only where it is
+ * stored, in the residual's type: the norm is that of the sum before.  Groups
+ * are 128 values (the last one what is left) or the row.  A group of zeros has
+ * scale 0 and codes 0; one that holds a NaN or whose y does has scale NaN.
+ * Squares past float32's range do not matter; sums h past it are infinite.
+ *
+ *   x               device bf16, 16-byte aligned, rows x_stride elements
+ *                   apart (a multiple of 8; strides are not used with one row)
+ *   residual_type   MLA_RESIDUAL_NONE (residual and residual_out are not
+ *                   used), _BF16 or _F32
+ *   residual        device, 16-byte aligned, rows residual_stride elements
+ *                   apart (16 bytes' multiple)
+ *   residual_out    likewise; may be residual with the same stride, else
+ *                   no element of it may be in another argument
+ *   weight          device bf16 [dim], 16-byte aligned
+ *   dim             a multiple of 8, 8..16384 (more: MLA_ERR_UNSUPPORTED)
+ *   group           128, or 0: the row (others: MLA_ERR_UNSUPPORTED)
+ *   eps             > 0
+ *   codes           device e4m3 [n_tokens, dim], 8-byte aligned
+ *   scales          device float [n_tokens, ceil(dim / group) or 1]
+ * n_tokens == 0 is a no-op.
+ */
+typedef enum { MLA_RESIDUAL_NONE = 0, MLA_RESIDUAL_BF16 = 1, MLA_RESIDUAL_F32 = 2 } mla_residual_t;
+mla_status_t mla_add_norm_quant(const uint16_t* x, int64_t x_stride, mla_residual_t residual_type,
+                                const void* residual, int64_t residual_stride, void* residual_out,
+                                int64_t residual_out_stride, const uint16_t* weight, int64_t n_tokens, int dim,
+                                int group, float eps, uint8_t* codes, float* scales, mla_stream_t stream);
+
+/*
+ * Products of a few tokens with matrices of 4-bit weights, one for each of
+ * `groups` (1: a projection of the token; the heads: each head's own):
+ *
+ *   out[t,g,n] = weight_scale[g] * sum_k x[t,g,k] * code[g,n,k] * scale[g,n,k/16]
+ *
+ * with the format of the cached latents: e2m1 codes, element 2i in the low
+ * nibble of byte i, and one e4m3 scale per 16.  x is bf16, or e4m3 codes with
+ * float scales as mla_add_norm_quant writes them.  Products are exact f16
+ * operands added up in float32 (a bf16 x loses what lies 2^-39 below the largest of
+ * its 128); the same call gives the same bits.  The weights are read once for
+ * up to 32 tokens (more tokens: once per 32).
+ *
+ *   x               device bf16 or e4m3, 16-byte aligned; group g of token t
+ *                   starts at t * token stride + g * group stride (elements,
+ *                   16 bytes' multiples; that of an axis with one entry is
+ *                   not used)
+ *   x_scales        device float [n_tokens, groups, x_scale_groups] (e4m3 only)
+ *   x_scale_groups  ceil(k / 128): one per 128 values; or 1: one per row
+ *   codes           device [groups, n, k / 2] bytes, 16-byte aligned
+ *   scales          device e4m3 [groups, n, k / 16], 2-byte aligned
+ *   weight_scale    device float [groups], or NULL: 1
+ *   k               a multiple of 32 (odd multiples of 16: MLA_ERR_UNSUPPORTED)
+ *   out             device bf16 or float, strides as x's, in elements (any);
+ *                   no two rows may share an element (checked)
+ *   groups          at most 65,535; n_tokens at most 2,097,120 (more:
+ *                   MLA_ERR_UNSUPPORTED)
+ * n_tokens, groups or n == 0 is a no-op.
+ */
+typedef enum { MLA_X_BF16 = 0, MLA_X_E4M3 = 1 } mla_x_type_t;
+typedef enum { MLA_OUT_BF16 = 0, MLA_OUT_F32 = 1 } mla_out_type_t;
+mla_status_t mla_fp4_matvec(const void* x, mla_x_type_t x_type, int64_t x_token_stride, int64_t x_group_stride,
+                            const float* x_scales, int x_scale_groups, const uint8_t* codes, const uint8_t* scales,
+                            const float* weight_scale, int64_t n_tokens, int groups, int n, int k, void* out,
+                            mla_out_type_t out_type, int64_t out_token_stride, int64_t out_group_stride,
+                            mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,7 @@ __all__ = [
     "mla_sparse_decode_staged", "mla_sparse_decode_mtp_workspace_size", "mla_sparse_decode_mtp",
     "mla_block_table_extend", "mla_qk_norm_rope", "mla_kv_norm_rope_append", "mla_window_decode_workspace_size",
     "mla_window_decode", "mla_prefix_decode_workspace_size", "mla_prefix_decode",
+    "mla_add_norm_quant", "mla_fp4_matvec",
 ]
 
 MLA_KV_NVFP4 = 0
@@ -85,6 +86,9 @@ SIGNATURES = {
     "mla_prefix_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "mla_prefix_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F32,
                                  _I32, _P, _P, _P, _SZ, _P]),
+    "mla_add_norm_quant": (_I32, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _F32, _P, _P, _P]),
+    "mla_fp4_matvec": (_I32, [_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I32, _I64, _I64,
+                              _P]),
 }
 
 
@@ -687,3 +691,115 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
                                     float(softmax_scale), fmt, _at(out), _at(lse), _at(workspace), ws_bytes,
                                     _on(stream, device)))
     return out, lse
+
+
+# --------------------------------------------------------------------- around the attention of a layer
+def _rows(t, dtype, name):
+    """Row stride of a [n, dim] tensor whose last axis is contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel() > 0):
+        raise ValueError(f"{name} must be [n, dim] with a contiguous last axis")
+    return t.stride(0)
+
+
+def _bytes(t, name):
+    """A contiguous tensor of e4m3 values, as float8_e4m3fn or bytes."""
+    if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+        raise TypeError(f"{name}: expected torch.float8_e4m3fn or torch.uint8, got {t.dtype}")
+    return _contig(t, t.dtype, name)
+
+
+def mla_add_norm_quant(x, weight, residual=None, eps=1e-6, group=128, codes=None, scales=None, residual_out=None,
+                       stream=None):
+    """h = x + residual, its norm times weight, and that in e4m3 with a float
+    scale per 128 values (group=128) or per row (group=0).  x bf16 [n, D],
+    residual bf16 or float32 [n, D] or None; rows may be strided.  Returns
+    (codes float8_e4m3fn [n, D], scales [n, ceil(D / 128) or 1], h in the
+    residual's type or None); residual_out may be residual."""
+    device = _here(x, weight, residual, codes, scales, None if residual is None else residual_out)
+    x_stride = _rows(x, torch.bfloat16, "x")
+    n, dim = x.shape
+    if _contig(weight, torch.bfloat16, "weight").numel() != dim:
+        raise ValueError(f"weight must have one value for each of {dim} dims")
+    _c_int(group, "group")
+    res_type = res_stride = out_stride = 0
+    if residual is not None:
+        if residual.dtype is not torch.bfloat16 and residual.dtype is not torch.float32:
+            raise TypeError(f"residual: expected torch.bfloat16 or torch.float32, got {residual.dtype}")
+        res_type = 1 if residual.dtype is torch.bfloat16 else 2
+        res_stride = _rows(residual, residual.dtype, "residual")
+        if residual_out is None:
+            residual_out = _new(residual, (n, dim), residual.dtype, stream)
+        out_stride = _rows(residual_out, residual.dtype, "residual_out")
+        if residual.shape != x.shape or residual_out.shape != x.shape:
+            raise ValueError("residual and residual_out must be shaped like x")
+    if codes is None:
+        codes = _new(x, (n, dim), torch.float8_e4m3fn, stream)
+    elif _bytes(codes, "codes").shape != x.shape:
+        raise ValueError("codes must be shaped like x")
+    scales = _take(scales, (n, -(-dim // group) if group > 0 else 1), torch.float32, "scales", x, stream)
+    _check("mla_add_norm_quant",
+           load().mla_add_norm_quant(x.data_ptr(), x_stride, res_type, _at(residual), res_stride,
+                                     None if residual is None else residual_out.data_ptr(), out_stride,
+                                     weight.data_ptr(), n, dim, group, float(eps), codes.data_ptr(), scales.data_ptr(),
+                                     _on(stream, device)))
+    return codes, scales, None if residual is None else residual_out
+
+
+def _token_groups(t, what):
+    """(token stride, group stride) of [T, K] or [T, G, K] with a contiguous last axis."""
+    strides = t.stride()
+    if len(strides) not in (2, 3) or (strides[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0):
+        raise ValueError(f"{what} must be [T, K] or [T, G, K] with a contiguous last axis")
+    return strides[0], strides[1] if len(strides) == 3 else 0
+
+
+def mla_fp4_matvec(x, codes, scales, weight_scale=None, x_scales=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Products of T tokens with 4-bit weights.  x [T, K] with codes uint8 [N,
+    K / 2] and scales e4m3 [N, K / 16], or x [T, G, K] with a matrix for each
+    group: codes [G, N, K / 2], scales [G, N, K / 16].  x bf16, or float8_e4m3fn
+    with x_scales float32 [T(, G), ceil(K / 128) or 1]; weight_scale float32, one
+    for each matrix, or None.  Returns out [T, N] or [T, G, N], bf16 or float32."""
+    device = _here(x, codes, scales, weight_scale, x_scales, out)
+    x_token, x_group = _token_groups(x, "x")
+    shape = x.shape
+    tokens, k = shape[0], shape[-1]
+    groups = shape[1] if len(shape) == 3 else 1
+    _contig(codes, torch.uint8, "codes")
+    _bytes(scales, "scales")
+    if codes.dim() != len(shape) or codes.shape[-1] * 2 != k or k % 16 != 0 or \
+            (len(shape) == 3 and codes.shape[0] != groups):
+        raise ValueError(f"codes {tuple(codes.shape)} do not fit x {tuple(shape)}: [N, K / 2] or [G, N, K / 2]")
+    n = codes.shape[-2]
+    if scales.shape != (*codes.shape[:-1], k // 16):
+        raise ValueError("scales must have one value for 16 codes")
+    if weight_scale is not None and _contig(weight_scale, torch.float32, "weight_scale").numel() != groups:
+        raise ValueError(f"weight_scale must have one value for each of {groups} matrices")
+    scale_groups = 0
+    if x.dtype is torch.float8_e4m3fn:
+        if x_scales is None:
+            raise ValueError("x in 8 bits needs x_scales")
+        _contig(x_scales, torch.float32, "x_scales")
+        scale_groups = x_scales.shape[-1] if x_scales.dim() > 0 else 0
+        if x_scales.shape[:-1] != shape[:-1] or scale_groups not in (1, -(-k // 128)):
+            raise ValueError("x_scales must have one value for 128 of x's, or one for each of its rows")
+    elif x.dtype is not torch.bfloat16:
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float8_e4m3fn, got {x.dtype}")
+    elif x_scales is not None:
+        raise ValueError("x_scales belong to x in 8 bits")
+    if out is None:
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+            raise TypeError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
+        out = _new(x, (*shape[:-1], n), out_dtype, stream)
+    elif out.shape != (*shape[:-1], n):
+        raise ValueError(f"out: expected shape {(*shape[:-1], n)}, got {tuple(out.shape)}")
+    elif out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise TypeError(f"out: expected torch.bfloat16 or torch.float32, got {out.dtype}")
+    out_token, out_group = _token_groups(out, "out")
+    _check("mla_fp4_matvec",
+           load().mla_fp4_matvec(x.data_ptr(), 1 if scale_groups else 0, x_token, x_group, _at(x_scales), scale_groups,
+                                 codes.data_ptr(), scales.data_ptr(), _at(weight_scale), tokens, groups, n, k,
+                                 out.data_ptr(), 1 if out.dtype is torch.float32 else 0, out_token, out_group,
+                                 _on(stream, device)))
+    return out

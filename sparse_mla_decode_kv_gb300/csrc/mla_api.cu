@@ -176,6 +176,8 @@ mla_status_t check_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t
   return MLA_OK;
 }
 
+constexpr int kMaxNormDim = 16384;
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -735,6 +737,91 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
   const DensePlan plan =
       plan_dense_decode(batch, q_len, num_heads, own_rows(max_blocks_per_req, max_context_len), prefix_len);
   return run_dense(fmt, a, plan, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mla_status_t mla_add_norm_quant(const uint16_t* x, int64_t x_stride, mla_residual_t residual_type,
+                                const void* residual, int64_t residual_stride, void* residual_out,
+                                int64_t residual_out_stride, const uint16_t* weight, int64_t n_tokens, int dim,
+                                int group, float eps, uint8_t* codes, float* scales, mla_stream_t stream) {
+  if (n_tokens < 0 || dim < 8 || dim % 8 != 0 || !(eps > 0.f) || !std::isfinite(eps)) return MLA_ERR_INVALID_ARG;
+  if (residual_type != MLA_RESIDUAL_NONE && residual_type != MLA_RESIDUAL_BF16 && residual_type != MLA_RESIDUAL_F32)
+    return MLA_ERR_INVALID_ARG;
+  if (group < 0 || group % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if ((group != 0 && group != 128) || dim > kMaxNormDim) return MLA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MLA_OK;
+  if (!x || !weight || !codes || !scales) return MLA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(codes, 8) || !aligned(scales, 4)) return MLA_ERR_INVALID_ARG;
+  if (n_tokens > 1 && x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (residual_type != MLA_RESIDUAL_NONE) {
+    if (!residual || !residual_out || !aligned(residual, 16) || !aligned(residual_out, 16)) return MLA_ERR_INVALID_ARG;
+    const int unit = residual_type == MLA_RESIDUAL_BF16 ? 8 : 4;  // 16 bytes
+    if (n_tokens > 1 && (residual_stride % unit != 0 || residual_out_stride % unit != 0 || residual_out_stride < dim ||
+                         (residual == residual_out && residual_stride != residual_out_stride)))
+      return MLA_ERR_INVALID_ARG;
+  }
+  AddNormArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.residual_type = residual_type;
+  a.residual = residual;
+  a.res_stride = residual_stride;
+  a.residual_out = residual_out;
+  a.res_out_stride = residual_out_stride;
+  a.weight = weight;
+  a.tokens = n_tokens;
+  a.dim = dim;
+  a.group = group;
+  a.scale_groups = group == 0 ? 1 : (dim + group - 1) / group;
+  a.eps = eps;
+  a.inv_dim = 1.f / static_cast<float>(dim);
+  a.codes = codes;
+  a.scales = scales;
+  return cuda_status(launch_add_norm_quant(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mla_status_t mla_fp4_matvec(const void* x, mla_x_type_t x_type, int64_t x_token_stride, int64_t x_group_stride,
+                            const float* x_scales, int x_scale_groups, const uint8_t* codes, const uint8_t* scales,
+                            const float* weight_scale, int64_t n_tokens, int groups, int n, int k, void* out,
+                            mla_out_type_t out_type, int64_t out_token_stride, int64_t out_group_stride,
+                            mla_stream_t stream) {
+  if (n_tokens < 0 || groups < 0 || n < 0 || k < 16 || k % 16 != 0) return MLA_ERR_INVALID_ARG;
+  if ((x_type != MLA_X_BF16 && x_type != MLA_X_E4M3) || (out_type != MLA_OUT_BF16 && out_type != MLA_OUT_F32))
+    return MLA_ERR_INVALID_ARG;
+  const int pieces = (k - 1) / 128 + 1;
+  if (x_type == MLA_X_E4M3 && x_scale_groups != 1 && x_scale_groups != pieces) return MLA_ERR_INVALID_ARG;
+  if (k % 32 != 0 || groups > 65535 || n_tokens > 32 * 65535) return MLA_ERR_UNSUPPORTED;
+  if (n_tokens == 0 || groups == 0 || n == 0) return MLA_OK;
+  if (!x || !codes || !scales || !out) return MLA_ERR_INVALID_ARG;
+  const int unit = x_type == MLA_X_BF16 ? 8 : 16;  // 16 bytes
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(weight_scale, 4) ||
+      !aligned(out, out_type == MLA_OUT_BF16 ? 2 : 4))
+    return MLA_ERR_INVALID_ARG;
+  if ((n_tokens > 1 && x_token_stride % unit != 0) || (groups > 1 && x_group_stride % unit != 0))
+    return MLA_ERR_INVALID_ARG;
+  if (x_type == MLA_X_E4M3 && (!x_scales || !aligned(x_scales, 4))) return MLA_ERR_INVALID_ARG;
+  // no two rows of the output may share an element
+  if ((n_tokens > 1 && out_token_stride < n) || (groups > 1 && out_group_stride < n) ||
+      rows_overlap(n_tokens, out_token_stride, groups, out_group_stride, n))
+    return MLA_ERR_INVALID_ARG;
+  MatvecArgs a{};
+  a.x = x;
+  a.x_codes = x_type == MLA_X_E4M3;
+  a.x_token = x_token_stride;
+  a.x_group = x_group_stride;
+  a.x_scales = x_scales;
+  a.x_scale_groups = x_scale_groups;
+  a.codes = codes;
+  a.scales = scales;
+  a.weight_scale = weight_scale;
+  a.tokens = n_tokens;
+  a.groups = groups;
+  a.n = n;
+  a.k = k;
+  a.out = out;
+  a.out_float = out_type == MLA_OUT_F32;
+  a.out_token = out_token_stride;
+  a.out_group = out_group_stride;
+  return cuda_status(launch_fp4_matvec(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -177,6 +177,49 @@ struct NormRopeArgs {
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 
+// Residual's addition, norm and e4m3 output (add_norm_quant.cu).
+struct AddNormArgs {
+  const uint16_t* x;
+  int64_t x_stride;  // elements, as the others
+  int residual_type;  // 0 none, 1 bf16, 2 float
+  const void* residual;
+  int64_t res_stride;
+  void* residual_out;
+  int64_t res_out_stride;
+  const uint16_t* weight;
+  int64_t tokens;
+  int dim;
+  int group;         // 128, or 0: the row
+  int scale_groups;  // scales per row
+  float eps;
+  float inv_dim;
+  uint8_t* codes;  // [tokens, dim]
+  float* scales;   // [tokens, scale_groups]
+};
+cudaError_t launch_add_norm_quant(const AddNormArgs& a, cudaStream_t stream);
+
+// Products with 4-bit weights (fp4_matvec.cu).
+struct MatvecArgs {
+  const void* x;  // bf16, or e4m3 codes
+  bool x_codes;
+  int64_t x_token, x_group;  // strides in elements
+  const float* x_scales;     // [tokens, groups, x_scale_groups], codes only
+  int x_scale_groups;        // 1 or ceil(k / 128)
+  const uint8_t* codes;      // [groups, n, k / 2]
+  const uint8_t* scales;     // [groups, n, k / 16]
+  const float* weight_scale;  // [groups] or null
+  int64_t tokens;
+  int groups;
+  int n;
+  int k;
+  void* out;
+  bool out_float;
+  int64_t out_token, out_group;
+  // set by the launch
+  int row_warps, splits;
+};
+cudaError_t launch_fp4_matvec(MatvecArgs a, cudaStream_t stream);
+
 // Indexer and top-k.
 size_t topk_workspace_bytes(int batch, int max_context_len, int topk);
 cudaError_t launch_topk(const float* scores, int64_t row_stride, const int32_t* context_lens, int batch, int topk,
