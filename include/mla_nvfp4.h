@@ -89,7 +89,7 @@ mla_status_t mla_last_cuda_error(int* cuda_err);
 
 /* Reads (and, if `clear` is nonzero, resets) the device fault word of the
  * current device: bit 0 = a decode wait ran out, bit 1 = an indexer or top-k
- * wait ran out.  Synchronises `stream`.  A nonzero word means some output of
+ * wait ran out, bit 2 = a wait of the prompt attention ran out.  Synchronises `stream`.  A nonzero word means some output of
  * an earlier call is incomplete. */
 mla_status_t mla_device_fault(unsigned int* word, int clear, mla_stream_t stream);
 
@@ -560,6 +560,58 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
                                const int32_t* context_lens, int batch, int q_len, int num_heads, int block_size,
                                int max_context_len, float softmax_scale, mla_kv_format_t fmt, uint16_t* out,
                                float* lse, void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * Attention over whole prompts, packed one behind another.  Sequence b has the
+ * query tokens query_start[b] .. query_start[b + 1] - 1 and the keys and values
+ * kv_start[b] .. kv_start[b + 1] - 1 (nq and nk of them); its queries are the
+ * last nq of its nk positions: query token i sees
+ *
+ *   causal      t < nk - nq + i + 1      (nothing where that is not positive)
+ *   otherwise   every t < nk
+ *
+ *   out = sum_t softmax_t(softmax_scale * q . k_t) v_t,   lse = the natural
+ *   logarithm of the softmax's denominator
+ *
+ * with query head h using key head h / (num_heads / num_kv_heads).  A token that
+ * sees nothing gives 0 and -inf.  Prompts, their later chunks behind earlier
+ * keys, drafts and single tokens are the same call.  Scores, softmax statistics
+ * and sums are float32; a weight enters the product as bf16 (off by at most
+ * 2^-8 of itself).  What a token does not see never reaches its output, be it
+ * infinite or NaN.
+ *
+ *   q             device bf16 [q_tokens, num_heads, qk_dim]
+ *   k, v          device bf16 [kv_tokens, num_kv_heads, qk_dim / v_dim]; not
+ *                 read if kv_tokens is 0
+ *   out           device bf16 [q_tokens, num_heads, v_dim]; tokens before the
+ *                 first sequence and behind the last are not written
+ *   strides       elements, multiples of 8; that of an axis with one entry is
+ *                 not used; no two rows of out may share an element (checked).
+ *                 All four tensors 16-byte aligned
+ *   query_start, kv_start   device int32 [batch + 1], not decreasing; values
+ *                 outside [0, q_tokens] or [0, kv_tokens] are cut to it
+ *   qk_dim        a multiple of 8, 8..192; v_dim 8..128 (more:
+ *                 MLA_ERR_UNSUPPORTED)
+ *   num_heads     a multiple of num_kv_heads, at most 128 of them for each
+ *                 (more: MLA_ERR_UNSUPPORTED)
+ *   softmax_scale finite, of either sign
+ *   lse           device float [q_tokens, num_heads], or NULL
+ *   workspace     at least mla_prompt_attention_workspace_size(...) bytes,
+ *                 256-byte aligned (that size depends on the current device
+ *                 and may be 0); contents on entry do not matter; calls that
+ *                 may run at the same time need one each
+ * batch == 0 or q_tokens == 0 is a no-op.  At most 2^31 - 256 tokens.
+ */
+size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
+                                           int num_kv_heads, int v_dim);
+mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* k,
+                                  int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                                  int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,
+                                  const int32_t* kv_start, int batch, int64_t q_tokens, int64_t kv_tokens,
+                                  int num_heads, int num_kv_heads, int qk_dim, int v_dim, int causal,
+                                  float softmax_scale, uint16_t* out, int64_t out_token_stride,
+                                  int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                                  mla_stream_t stream);
 
 /*
  * The residual's addition, the norm behind it, and its output in 8 bits.  For

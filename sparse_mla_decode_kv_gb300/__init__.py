@@ -25,7 +25,7 @@ __all__ = [
     "mla_sparse_decode_staged", "mla_sparse_decode_mtp_workspace_size", "mla_sparse_decode_mtp",
     "mla_block_table_extend", "mla_qk_norm_rope", "mla_kv_norm_rope_append", "mla_window_decode_workspace_size",
     "mla_window_decode", "mla_prefix_decode_workspace_size", "mla_prefix_decode",
-    "mla_add_norm_quant", "mla_fp4_matvec",
+    "mla_prompt_attention_workspace_size", "mla_prompt_attention", "mla_add_norm_quant", "mla_fp4_matvec",
 ]
 
 MLA_KV_NVFP4 = 0
@@ -86,6 +86,9 @@ SIGNATURES = {
     "mla_prefix_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "mla_prefix_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F32,
                                  _I32, _P, _P, _P, _SZ, _P]),
+    "mla_prompt_attention_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I32]),
+    "mla_prompt_attention": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32, _I32,
+                                    _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "mla_add_norm_quant": (_I32, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _F32, _P, _P, _P]),
     "mla_fp4_matvec": (_I32, [_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I32, _I64, _I64,
                               _P]),
@@ -693,7 +696,50 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
     return out, lse
 
 
-# --------------------------------------------------------------------- around the attention of a layer
+# --------------------------------------------------------------------- prompts, and around the attention of a layer
+def mla_prompt_attention_workspace_size(q_tokens: int, kv_tokens: int, batch: int, num_heads: int, num_kv_heads: int,
+                                        v_dim: int) -> int:
+    return int(load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim))
+
+
+def mla_prompt_attention(q, k, v, query_start, kv_start, softmax_scale, causal=True, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Attention of packed sequences: b's query tokens are query_start[b] ..
+    query_start[b + 1] - 1 of q [Tq, H, D], its keys and values kv_start[b] ..
+    kv_start[b + 1] - 1 of k [Tk, Hk, D], v [Tk, Hk, Dv], its queries the last of
+    those positions.  All bf16 with any strides over tokens and heads, the starts
+    int32 [B + 1].  Returns (out bf16 [Tq, H, Dv], lse or None)."""
+    device = _here(q, k, v, query_start, kv_start, out, lse, workspace)
+    q_token, q_head, _ = _head_strides(q, "q")
+    k_token, k_head, _ = _head_strides(k, "k")
+    v_token, v_head, _ = _head_strides(v, "v")
+    q_tokens, heads, dk = q.shape
+    kv_tokens, kv_heads, dv = v.shape
+    if k.shape != (kv_tokens, kv_heads, dk):
+        raise ValueError("k [Tk, Hk, D] and v [Tk, Hk, Dv] must have the same tokens and heads, and k the dims of q")
+    batch = _contig(query_start, torch.int32, "query_start").numel() - 1
+    if batch < 0 or _contig(kv_start, torch.int32, "kv_start").numel() != batch + 1:
+        raise ValueError("query_start and kv_start must have one entry for each sequence and one more")
+    if out is None:
+        out = _new(q, (q_tokens, heads, dv), torch.bfloat16, stream)
+    elif out.shape != (q_tokens, heads, dv):
+        raise ValueError(f"out: expected shape {(q_tokens, heads, dv)}, got {tuple(out.shape)}")
+    out_token, out_head, _ = _head_strides(out, "out")
+    if lse is not None:
+        _take(lse, (q_tokens, heads), torch.float32, "lse", q, stream)
+    if workspace is None:
+        need = load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, heads, kv_heads, dv)
+        workspace = _new(q, (need,), torch.uint8, stream) if need > 0 else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("mla_prompt_attention",
+           load().mla_prompt_attention(q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head, v.data_ptr(),
+                                       v_token, v_head, query_start.data_ptr(), kv_start.data_ptr(), batch, q_tokens,
+                                       kv_tokens, heads, kv_heads, dk, dv, int(causal), float(softmax_scale),
+                                       out.data_ptr(), out_token, out_head, _at(lse), _at(workspace), ws_bytes,
+                                       _on(stream, device)))
+    return out, lse
+
+
 def _rows(t, dtype, name):
     """Row stride of a [n, dim] tensor whose last axis is contiguous."""
     if t.dtype is not dtype:

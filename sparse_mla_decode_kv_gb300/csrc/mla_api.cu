@@ -177,6 +177,7 @@ mla_status_t check_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t
 }
 
 constexpr int kMaxNormDim = 16384;
+constexpr int64_t kMaxTokens = 0x7FFFFF00;  // of a packed batch: a tile past the last still has a 32-bit number
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -282,6 +283,20 @@ bool encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void
   const cuuint32_t estr[2] = {1u, 1u};
   return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t heads, uint64_t rows,
+                          uint64_t head_stride, uint64_t row_stride, uint32_t box_heads, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t any = (2 * inner + 15) / 16 * 16;  // for an axis of one entry
+  const cuuint64_t dims[3] = {inner, heads, rows};
+  const cuuint64_t strides[2] = {heads > 1 ? head_stride : any, rows > 1 ? row_stride : any};
+  const cuuint32_t box[3] = {64u, box_heads, box_rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace mla
@@ -822,6 +837,82 @@ mla_status_t mla_fp4_matvec(const void* x, mla_x_type_t x_type, int64_t x_token_
   a.out_token = out_token_stride;
   a.out_group = out_group_stride;
   return cuda_status(launch_fp4_matvec(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
+                                           int num_kv_heads, int v_dim) {
+  if (q_tokens <= 0 || q_tokens > kMaxTokens || kv_tokens < 0 || kv_tokens > kMaxTokens || batch <= 0 ||
+      num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 128 || v_dim < 8)
+    return 0;
+  return plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim).workspace;
+}
+
+mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* k,
+                                  int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                                  int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,
+                                  const int32_t* kv_start, int batch, int64_t q_tokens, int64_t kv_tokens,
+                                  int num_heads, int num_kv_heads, int qk_dim, int v_dim, int causal,
+                                  float softmax_scale, uint16_t* out, int64_t out_token_stride,
+                                  int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                                  mla_stream_t stream) {
+  if (batch < 0 || q_tokens < 0 || kv_tokens < 0 || num_heads < 1 || num_kv_heads < 1 ||
+      num_heads % num_kv_heads != 0 || qk_dim < 8 || qk_dim % 8 != 0 || v_dim < 8 || v_dim % 8 != 0 ||
+      !std::isfinite(softmax_scale))
+    return MLA_ERR_INVALID_ARG;
+  if (qk_dim > 192 || v_dim > 128 || num_heads / num_kv_heads > 128 || q_tokens > kMaxTokens || kv_tokens > kMaxTokens)
+    return MLA_ERR_UNSUPPORTED;
+  if (batch == 0 || q_tokens == 0) return MLA_OK;
+  if (!q || !query_start || !kv_start || !out || (kv_tokens > 0 && (!k || !v))) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(query_start, 4) ||
+      !aligned(kv_start, 4) || !aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  // the stride of an axis of one entry is not used
+  if ((q_tokens > 1 && (q_token_stride % 8 || out_token_stride % 8)) ||
+      (num_heads > 1 && (q_head_stride % 8 || out_head_stride % 8)) ||
+      (kv_tokens > 1 && (k_token_stride % 8 || v_token_stride % 8)) ||
+      (num_kv_heads > 1 && (k_head_stride % 8 || v_head_stride % 8)))
+    return MLA_ERR_INVALID_ARG;
+  if ((q_tokens > 1 && out_token_stride < v_dim) || (num_heads > 1 && out_head_stride < v_dim) ||
+      rows_overlap(q_tokens, out_token_stride, num_heads, out_head_stride, v_dim))
+    return MLA_ERR_INVALID_ARG;
+  const PromptPlan plan = plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim);
+  if (plan.places * num_kv_heads * plan.splits > 0x7FFFFFFF || q_tokens * num_heads > 0x7FFFFFFF)
+    return MLA_ERR_UNSUPPORTED;
+  if (plan.workspace > 0) {
+    if (workspace_bytes < plan.workspace) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  }
+  PromptArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.q_tokens = static_cast<int>(q_tokens);
+  a.kv_tokens = static_cast<int>(kv_tokens);
+  a.batch = batch;
+  a.q_start = query_start;
+  a.kv_start = kv_start;
+  a.heads = num_heads;
+  a.kv_heads = num_kv_heads;
+  a.dk = qk_dim;
+  a.dv = v_dim;
+  a.causal = causal != 0;
+  a.negate = softmax_scale < 0.f;
+  // a scale of 0 makes all weights equal, but must keep what is masked at -infinity
+  a.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 1.401298464324817e-45f);
+  a.out = out;
+  a.out_token = out_token_stride;
+  a.out_head = out_head_stride;
+  a.lse = lse;
+  bool described = false;
+  const cudaError_t e =
+      launch_prompt_attention(a, plan, workspace, reinterpret_cast<cudaStream_t>(stream), &described);
+  return described ? cuda_status(e) : MLA_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@ constexpr int kIdxDim = 128;               // indexer key width (e4m3)
 // mla_api.cu whose address kernels receive as an argument).
 constexpr unsigned int kFaultDecodeWait = 1u;
 constexpr unsigned int kFaultIndexerWait = 2u;
+constexpr unsigned int kFaultPromptWait = 4u;
 // Poll budget of the back-off phase of a bounded wait (each poll sleeps a
 // few microseconds): about a second in total, with the hinted phase before
 // it, far beyond any legitimate wait in these kernels (microseconds).  Polls

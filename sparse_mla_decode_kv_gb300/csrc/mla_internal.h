@@ -28,6 +28,12 @@ bool encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void
                           uint64_t rows, uint64_t row_stride, uint32_t box_inner, uint32_t box_rows,
                           CUtensorMapSwizzle swizzle);
 
+// The same over bf16 values [rows][heads][inner] with strides of the two outer axes
+// in bytes (not used for an axis of one entry); box 64 x box_heads x box_rows, the
+// 128-byte swizzle.
+bool encode_tensor_map_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t heads, uint64_t rows,
+                          uint64_t head_stride, uint64_t row_stride, uint32_t box_heads, uint32_t box_rows);
+
 cudaError_t launch_quantize_append(const uint16_t* latent, const uint16_t* rope, const int64_t* slot_mapping,
                                    int64_t n_tokens, void* pool, int64_t num_blocks, int64_t block_stride, int fmt,
                                    cudaStream_t stream);
@@ -176,6 +182,40 @@ struct NormRopeArgs {
   int fmt;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// Attention over packed prompts (prompt_attention.cu).
+struct PromptPlan {
+  int64_t places;    // of pairs of row tiles, per key head
+  int splits;        // CTAs per pair along the keys
+  size_t workspace;  // bytes of partials, 0 for a single slice
+};
+struct PromptArgs {
+  const uint16_t* q;  // bf16 [q_tokens, heads, dk], strides in elements
+  const uint16_t* k;  // [kv_tokens, kv_heads, dk]
+  const uint16_t* v;  // [kv_tokens, kv_heads, dv]
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int q_tokens, kv_tokens;
+  int batch;
+  const int32_t* q_start;   // [batch + 1]
+  const int32_t* kv_start;  // [batch + 1]
+  int heads, kv_heads, dk, dv;
+  bool causal;
+  bool negate;       // a negative scale: the products are negated
+  float scale_log2;  // > 0
+  uint16_t* out;     // [q_tokens, heads, dv], strides in elements
+  int64_t out_token, out_head;
+  float* lse;  // [q_tokens, heads] or null
+  // set by the launch from the plan
+  int group, splits, places;
+  float* part_o;
+  float* part_lse;
+  unsigned int* fault_word;
+};
+PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch, int heads, int kv_heads, int dv);
+// *described: whether the tensors' strides can be described to the copy engine; nothing
+// is launched if not.
+cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* workspace, cudaStream_t stream,
+                                    bool* described);
 
 // Residual's addition, norm and e4m3 output (add_norm_quant.cu).
 struct AddNormArgs {
