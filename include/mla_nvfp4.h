@@ -89,8 +89,8 @@ mla_status_t mla_last_cuda_error(int* cuda_err);
 
 /* Reads (and, if `clear` is nonzero, resets) the device fault word of the
  * current device: bit 0 = a decode wait ran out, bit 1 = an indexer or top-k
- * wait ran out, bit 2 = a wait of the prompt attention ran out.  Synchronises `stream`.  A nonzero word means some output of
- * an earlier call is incomplete. */
+ * wait ran out, bit 2 = a wait of the prompt attention ran out.  Synchronises
+ * `stream`.  A nonzero word means some output of an earlier call is incomplete. */
 mla_status_t mla_device_fault(unsigned int* word, int clear, mla_stream_t stream);
 
 /*

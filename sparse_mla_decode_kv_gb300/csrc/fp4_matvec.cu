@@ -11,15 +11,15 @@
 // then multiplied by the token's factor for them (its scale, or the power of
 // two back) into a float total.
 //
-// Split.  A warp has 16 MT rows of weights as the A operand and 8 NT tokens as
-// B (m16n8k16).  Which 16 values of k an MMA adds up is free as long as both
-// operands agree: lane t of a row's four has the 32 consecutive codes 32 t ..
-// of each 128, so a lane's codes are one 16-byte load, its scales one 2-byte
-// load, and every group's scale is needed by one lane only.  The tokens are laid
-// out in shared memory in the order in which the lanes read them.  A CTA is WR x
-// WK warps: rows, and 128-value pieces of k in turn; up to 8 CTAs of a cluster
-// have slices of k.  Their sums are joined in shared memory in one order, so a
-// call gives the same bits every time.
+// Split.  A CTA has R consecutive rows, as many as make the CTAs equal, and up to 8 CTAs of a cluster a slice of k each: WR warps share the rows,
+// WK the slice.  A warp has 16 rows as the A operand and 8 NT tokens as B
+// (m16n8k16), 128 values of k (a piece) a step.  Which 16 values of k an MMA adds
+// up is free as long as both operands agree: lane t of a row's four has the 32
+// consecutive codes 32 t .. of a piece, so a lane's codes are one 16-byte load, its
+// scales one 2-byte load, and every group's scale is needed by one lane only.  The
+// tokens lie in shared memory in the order in which the lanes read them.
+// Sums of warps and CTAs are joined in one order: a call gives the same bits
+// every time.
 //
 // Bound: HBM, 9/16 byte a weight.
 #include <cuda_bf16.h>
@@ -35,24 +35,26 @@
 namespace mla {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kPiece = 128;  // values of k per step of a warp
-// Tokens' values of one piece, in units of 8: [n-tile][4][8 tokens x 4 lanes],
-// the four 34 units apart so that a token's sixteen units fall into different banks
-// when they are written.
-constexpr int kUnitStride = 34;
-constexpr int kPieceUnits = 4 * kUnitStride;
+constexpr int kPiece = 128;    // values of k per step of a warp
+__host__ __device__ constexpr int stage_tasks(int nt) { return nt == 1 ? 256 : 512; }  // (piece, token) pairs of a stage
+constexpr int kMaxRows = 1024;  // of a CTA
+constexpr int kMaxSplits = 8;  // portable cluster size
+constexpr int kSmemBytes = 227 * 1024;
 
-__host__ __device__ constexpr int depth(int nt) { return nt == 1 ? 4 : 2; }  // pieces on their way in registers
-__host__ __device__ constexpr int stage_pieces(int nt) { return nt == 1 ? 32 : nt == 2 ? 16 : 8; }
-__host__ __device__ constexpr int piece_bytes(int nt) { return nt * (kPieceUnits * 16 + 8 * 4); }
-// Joined sums: [WK][tokens][rows + 4] floats over the place of the tokens.
-__host__ __device__ constexpr int sum_bytes(int mt, int nt) { return 8 * nt * (16 * mt + 4) * kWarps * 4; }
-__host__ __device__ constexpr int smem_bytes(int mt, int nt) {
-  const int a = stage_pieces(nt) * piece_bytes(nt), b = sum_bytes(mt, nt);
-  return a > b ? a : b;
+// By the tiles of 8 tokens: CTAs an SM that registers leave room for, and pieces whose
+// weights a warp loads at a time.
+__host__ __device__ constexpr int warp_bits(int nt) { return nt == 1 ? 3 : 4; }
+__host__ __device__ constexpr int resident(int nt) { return nt == 1 ? 3 : 1; }
+__host__ __device__ constexpr int batch(int nt) { return nt == 4 ? 2 : 4; }
+// Tokens' values of one piece, in units of 8: [n-tile][4][tokens x 4 lanes] with the
+// four 2 units further apart than that, so that a token's sixteen units fall into
+// different banks when they are written.  `toks` is a power of two, or 8 NT.
+__host__ __device__ constexpr int row_units(int nt, int toks) { return (nt > 1 ? 8 : toks) * 4 + 2; }
+__host__ __device__ constexpr int piece_bytes(int nt, int toks) {
+  return nt * 4 * row_units(nt, toks) * 16 + (toks < 4 ? 16 : 4 * toks);
 }
+// Joined sums: [WK][tokens][rows, and 4 to spread the banks] floats.
+__host__ __device__ constexpr int64_t sum_bytes(int toks, int wk, int64_t rows) { return wk * toks * (rows + 4) * 4; }
 
 struct Weights {  // one lane's part of 16 rows x 128 values: rows g and g + 8
   uint4 code[2];
@@ -66,211 +68,297 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t load_two(const uint8_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+// Starts bringing memory to L2 (both 16-byte aligned).
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+// The first product of a sum: nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
-template <int MT, int NT, bool kCodes>
-__global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint4* const s_x = reinterpret_cast<uint4*>(smem);
-  float* const s_mul = reinterpret_cast<float*>(smem + stage_pieces(NT) * NT * kPieceUnits * 16);
+template <int NT, bool kCodes>
+__global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_kernel(const MatvecArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTokens = 8 * NT;
-  constexpr int kDepth = depth(NT);
+  constexpr int kBatch = batch(NT);
+  constexpr int kWarpBits = warp_bits(NT), kThreads = 32 << kWarpBits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int wr = a.row_warps, wk = kWarps / wr;
-  const int split = blockIdx.x % a.splits;
-  const int rows_cta = 16 * MT * wr;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / a.splits) * rows_cta;
+  const int wr_bits = a.row_warps_bits, wk_bits = kWarpBits - wr_bits;
+  const int w_row = warp & ((1 << wr_bits) - 1), w_k = warp >> wr_bits, wk = 1 << wk_bits;
+  const int block = blockIdx.x / static_cast<unsigned>(a.splits), split = blockIdx.x - block * a.splits;
+  const int64_t row0 = static_cast<int64_t>(block) * a.rows;
+  const int rows_cta = static_cast<int>(min(static_cast<int64_t>(a.rows), a.n - row0));
   const int grp = blockIdx.y;
   const int64_t tok0 = static_cast<int64_t>(blockIdx.z) * kTokens;
   const int toks = static_cast<int>(min(static_cast<int64_t>(kTokens), a.tokens - tok0));
+
+  // this warp's rows: whole tiles of 16, spread over the warps
+  const int tiles = (rows_cta + 15) / 16;
+  const int tile0 = (tiles * w_row) >> wr_bits, n_tiles = ((tiles * (w_row + 1)) >> wr_bits) - tile0;
+  // the CTA's pieces of k, and of a stage of them this warp's
   const int pieces = (a.k + kPiece - 1) / kPiece;
-  const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * split / a.splits);
-  const int p1 = static_cast<int>(static_cast<int64_t>(pieces) * (split + 1) / a.splits);
-  const int w_row = warp % wr, w_k = warp / wr;
-  const int steps = (p1 - p0 + wk - 1) / wk;               // of every warp
-  const int stage_steps = stage_pieces(NT) / wk;           // of every warp with the same tokens in shared memory
+  const int p_lo = min(split * a.slice, pieces), p_hi = min(p_lo + a.slice, pieces);
+  auto stage_lo = [&](int s) { return p_lo + s * a.stage; };
+  auto stage_n = [&](int s) { return min(a.stage, p_hi - stage_lo(s)); };
+  auto share_lo = [&](int s) { return (stage_n(s) * w_k) >> wk_bits; };
+  auto share_n = [&](int s) { return ((stage_n(s) * (w_k + 1)) >> wk_bits) - share_lo(s); };
+  const int64_t code_row = a.k / 2, scale_row = a.k / 16;
 
-  // rows past the last read the last one's weights, their sums are not written
-  const uint8_t* code[MT][2];
-  const uint8_t* scale[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t r = min(row0 + 16 * (MT * w_row + m) + 8 * h + g, static_cast<int64_t>(a.n) - 1);
-      const int64_t at = static_cast<int64_t>(grp) * a.n + r;
-      code[m][h] = a.codes + at * (a.k / 2) + 16 * t;
-      scale[m][h] = a.scales + at * (a.k / 16) + 2 * t;
+  // The CTA's weights are on their way to L2 while the tokens are awaited and laid out,
+  // also while the kernel in front still runs (who writes them after that writes to L2).
+  // Whole rows of k alone, and scales where they begin at multiples of 16 bytes.
+  if (p_lo < p_hi) {
+    const int64_t k0 = static_cast<int64_t>(p_lo) * kPiece;
+    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(p_hi) * kPiece, static_cast<int64_t>(a.k)) - k0) / 2;
+    const bool with_scales = a.k % 256 == 0 && p_lo % 2 == 0 && p_hi % 2 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0;
+    for (int r = threadIdx.x; r < rows_cta; r += kThreads) {
+      const int64_t row = static_cast<int64_t>(grp) * a.n + row0 + r;
+      prefetch_l2(a.codes + row * code_row + k0 / 2, bytes);
+      if (with_scales) prefetch_l2(a.scales + row * scale_row + k0 / 16, bytes / 8);
     }
-  Weights buf[kDepth][MT];
-  auto fetch = [&](int step, Weights (&w)[MT]) {
-    const int p = p0 + w_k + wk * step;
-    const bool here = p < p1 && p * kPiece + 32 * t < a.k;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        w[m].code[h] = here ? load_stream(code[m][h] + static_cast<int64_t>(p) * (kPiece / 2)) : make_uint4(0, 0, 0, 0);
-        w[m].scale[h] = here ? *reinterpret_cast<const unsigned short*>(scale[m][h] + static_cast<int64_t>(p) * (kPiece / 16)) : 0;
-      }
-  };
-#pragma unroll
-  for (int i = 0; i < kDepth; ++i) fetch(i, buf[i]);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // The tokens of pieces [p0 + at, ...): half a warp has one token's piece, 8
-  // values a lane.
-  auto stage = [&](int at) {
-    const int count = min(stage_pieces(NT), p1 - p0 - at);
-    const int u = lane & 15;
-    const uint32_t half = lane & 16 ? 0xFFFF0000u : 0x0000FFFFu;  // the halves go round a different number of times
-    for (int i = threadIdx.x >> 4; i < count * toks; i += kThreads / 16) {
-      const int piece = i / toks, tok = i - piece * toks;
-      const int k0 = (p0 + at + piece) * kPiece + 8 * u;
-      const int64_t off = (tok0 + tok) * a.x_token + grp * a.x_group + k0;
-      uint32_t h[4] = {0, 0, 0, 0};
-      float mul = 1.f;
-      if constexpr (kCodes) {
-        if (k0 < a.k) {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + off);
-          uint32_t lo[2], hi[2];
-          e4m3x4_to_f16x2x2(v.x, lo);
-          e4m3x4_to_f16x2x2(v.y, hi);
-          h[0] = lo[0];
-          h[1] = lo[1];
-          h[2] = hi[0];
-          h[3] = hi[1];
-        }
-        if (u == 0) mul = a.x_scales[((tok0 + tok) * a.groups + grp) * a.x_scale_groups + (a.x_scale_groups > 1 ? p0 + at + piece : 0)];
-      } else {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (k0 < a.k) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + off);
-        uint32_t mx = bf16x8_absmax_bits(v);
+  // ---- tokens.  Half a warp has one token's piece, 8 values a lane.
+  const int tok_bits = toks <= 1 ? 0 : 32 - __clz(toks - 1);
+  const int tok_p = NT > 1 ? kTokens : 1 << tok_bits;  // tokens with a place
+  const int ru = row_units(NT, tok_p);
+  uint4* const s_x = reinterpret_cast<uint4*>(smem);
+  float* const s_mul = reinterpret_cast<float*>(smem + a.stage * NT * 4 * ru * 16);
+  float* const s_sum = reinterpret_cast<float*>(smem + a.stage * piece_bytes(NT, tok_p));  // [w_k][token][row]
+  const int pitch = a.rows + 4;
+  const int u = lane & 15;
+  const uint32_t half = lane & 16 ? 0xFFFF0000u : 0x0000FFFFu;  // the halves may go different ways
+  auto stage_tokens = [&](int s) {
+    const int lo = stage_lo(s), count = stage_n(s) << tok_bits;
+    constexpr int kAhead = 8;
+    constexpr int kRegs = kCodes ? 2 : 4;
+#pragma unroll 1
+    for (int i0 = threadIdx.x >> 4; i0 < count; i0 += kAhead * (kThreads / 16)) {
+      uint32_t raw[kAhead][kRegs];
+      float raw_mul[kCodes ? kAhead : 1];
 #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(half, mx, m));
-        const int shift = query_shift(mx);
-        const float up = pow2f(shift);
-        mul = pow2f(-shift);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * (kThreads / 16);
+        const int tok = i & ((1 << tok_bits) - 1), piece = lo + (i >> tok_bits);
+        const int64_t k0 = static_cast<int64_t>(piece) * kPiece + 8 * u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2 p = __floats2half2_rn(bf16_bits_to_f32(w[j] & 0xFFFFu) * up, bf16_bits_to_f32(w[j] >> 16) * up);
-          h[j] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int e = 0; e < kRegs; ++e) raw[j][e] = 0;
+        if constexpr (kCodes) raw_mul[j] = 0.f;
+        if (i < count && tok < toks && k0 < a.k) {
+          const int64_t off = (tok0 + tok) * a.x_token + grp * a.x_group + k0;
+          if constexpr (kCodes) {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + off);
+            raw[j][0] = w.x;
+            raw[j][1] = w.y;
+            raw_mul[j] = a.x_scales[((tok0 + tok) * a.groups + grp) * a.x_scale_groups + (a.x_scale_groups > 1 ? piece : 0)];
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + off);
+            raw[j][0] = w.x;
+            raw[j][1] = w.y;
+            raw[j][2] = w.z;
+            raw[j][3] = w.w;
+          }
         }
       }
-      const int nt = tok >> 3;
-      s_x[(piece * NT + nt) * kPieceUnits + (u & 3) * kUnitStride + (tok & 7) * 4 + (u >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
-      if (u == 0) s_mul[piece * kTokens + tok] = mul;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * (kThreads / 16);
+        const int tok = i & ((1 << tok_bits) - 1), slot = i >> tok_bits;
+        if (i >= count) continue;
+        uint32_t h[4];
+        float mul;
+        if constexpr (kCodes) {
+          uint32_t lo2[2], hi2[2];
+          e4m3x4_to_f16x2x2(raw[j][0], lo2);
+          e4m3x4_to_f16x2x2(raw[j][1], hi2);
+          h[0] = lo2[0];
+          h[1] = lo2[1];
+          h[2] = hi2[0];
+          h[3] = hi2[1];
+          mul = raw_mul[j];
+        } else {
+          uint32_t mx = bf16x8_absmax_bits(make_uint4(raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
+#pragma unroll
+          for (int m = 8; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(half, mx, m));
+          const int shift = query_shift(mx);
+          const float up = pow2f(shift);
+          mul = pow2f(-shift);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = raw[j][e];
+            const __half2 p = __floats2half2_rn(bf16_bits_to_f32(w & 0xFFFFu) * up, bf16_bits_to_f32(w >> 16) * up);
+            h[e] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+        }
+        s_x[((slot * NT + (tok >> 3)) * 4 + (u & 3)) * ru + (tok & 7) * 4 + (u >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (u == 0) s_mul[slot * tok_p + tok] = mul;
+      }
     }
   };
-
-  if (toks < kTokens) {  // the tokens that are not there are zeros
-    for (int i = threadIdx.x; i < stage_pieces(NT) * piece_bytes(NT) / 16; i += kThreads) s_x[i] = make_uint4(0, 0, 0, 0);
+  if (NT > 1 && toks < kTokens) {  // the tokens that are not there are zeros
+    for (int i = threadIdx.x; i < a.stage * piece_bytes(NT, tok_p) / 16; i += kThreads) s_x[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
-  float tot[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.f;
+  for (int i = threadIdx.x; i < wk * tok_p * pitch; i += kThreads) s_sum[i] = 0.f;
+  const bool x_here = NT > 1 || g < tok_p;      // else this lane's token (of B) has no place
+  const bool y_here = NT > 1 || 2 * t < tok_p;  // and its two tokens of the sums
 
-#pragma unroll 1
-  for (int s0 = 0; s0 < steps; s0 += kDepth) {
-    if (s0 % stage_steps == 0) {
-      if (s0 > 0) __syncthreads();
-      stage(s0 * wk);
-      __syncthreads();
+  float tot[NT][4];
+  // One piece: its weights and the tokens of place x (of factors m) into the sums.
+  auto add_piece = [&](const Weights& w, const uint4* x, const float* m) {
+    float acc[NT][4];
+    uint32_t sc[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h][0] = e4m3x2_to_f16x2(__byte_perm(w.scale[h], 0, 0x4400));
+      sc[h][1] = e4m3x2_to_f16x2(__byte_perm(w.scale[h], 0, 0x4411));
     }
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-      const int step = s0 + i;
-      if (step >= steps) break;
-      const int local = (step % stage_steps) * wk + w_k;
-      const bool here = p0 + w_k + wk * step < p1;  // uniform over the warp
-      if (here) {
-        float acc[MT][NT][4];
+    for (int j = 0; j < 4; ++j) {
+      uint4 b[NT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NT; ++n) {
+        b[n] = x[(n * 4 + j) * ru];
+        if (NT == 1 && !x_here) b[n] = make_uint4(0, 0, 0, 0);
+      }
+      const uint4 c0 = w.code[0], c1 = w.code[1];
+      uint32_t lo[4], hi[4];
+      e2m1x8_to_f16x2x4(j == 0 ? c0.x : j == 1 ? c0.y : j == 2 ? c0.z : c0.w, lo);
+      e2m1x8_to_f16x2x4(j == 0 ? c1.x : j == 1 ? c1.y : j == 2 ? c1.z : c1.w, hi);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+      for (int e = 0; e < 4; ++e) {
+        lo[e] = hmul2(lo[e], sc[0][j >> 1]);
+        hi[e] = hmul2(hi[e], sc[1][j >> 1]);
+      }
+      const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
-        uint32_t sc[MT][2][2];
+      for (int n = 0; n < NT; ++n) {
+        if (j == 0)
+          mma_f16_first(acc[n], a0, b[n].x, b[n].y);
+        else
+          mma_f16(acc[n], a0, b[n].x, b[n].y);
+        mma_f16(acc[n], a1, b[n].z, b[n].w);
+      }
+    }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n) {
+      // a token without a place meets another's factor, and sums of zeros
+      const float2 mul = NT > 1 || tok_p > 1 ? *reinterpret_cast<const float2*>(m + 8 * n) : make_float2(*m, 0.f);
+      tot[n][0] = fmaf(acc[n][0], mul.x, tot[n][0]);
+      tot[n][1] = fmaf(acc[n][1], mul.y, tot[n][1]);
+      tot[n][2] = fmaf(acc[n][2], mul.x, tot[n][2]);
+      tot[n][3] = fmaf(acc[n][3], mul.y, tot[n][3]);
+    }
+  };
+
+#pragma unroll 1
+  for (int st = 0; stage_lo(st) < p_hi; ++st) {
+    if (st > 0) __syncthreads();
+    stage_tokens(st);
+    __syncthreads();
+    const int n = share_n(st), lo = stage_lo(st) + share_lo(st);
+    // whole pieces, in batches; the rest one by one
+    const int whole = max(0, min(n, a.k / kPiece - lo)) / kBatch * kBatch;
+#pragma unroll 1
+    for (int tile = 0; tile < (n > 0 ? n_tiles : 0); ++tile) {
+      // rows past the CTA's last read that one's weights; their sums are not kept
+      const int r = 16 * (tile0 + tile) + g;
+      const uint8_t* code[2];
+      const uint8_t* scale[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t row = static_cast<int64_t>(grp) * a.n + row0 + min(r + 8 * h, rows_cta - 1);
+        code[h] = a.codes + row * code_row + static_cast<int64_t>(lo) * (kPiece / 2) + 16 * t;
+        scale[h] = a.scales + row * scale_row + static_cast<int64_t>(lo) * (kPiece / 16) + 2 * t;
+      }
+      const uint4* x = s_x + share_lo(st) * (NT * 4 * ru) + (x_here ? lane : 0);
+      const float* m = s_mul + share_lo(st) * tok_p + (y_here ? 2 * t : 0);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tot[i][e] = 0.f;
+      int p = 0;
+#pragma unroll 1
+      for (; p < whole; p += kBatch) {
+        Weights w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t two = buf[i][m].scale[h];
-            sc[m][h][0] = e4m3x2_to_f16x2((two & 0xFFu) * 0x0101u);
-            sc[m][h][1] = e4m3x2_to_f16x2((two >> 8) * 0x0101u);
+            w[i].code[h] = load_stream(code[h] + i * (kPiece / 2));
+            w[i].scale[h] = load_two(scale[h] + i * (kPiece / 16));
           }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 b[NT];
+        for (int i = 0; i < kBatch; ++i) add_piece(w[i], x + i * (NT * 4 * ru), m + i * tok_p);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) b[n] = s_x[(local * NT + n) * kPieceUnits + j * kUnitStride + lane];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint4 c0 = buf[i][m].code[0], c1 = buf[i][m].code[1];
-            uint32_t lo[4], hi[4];
-            e2m1x8_to_f16x2x4(j == 0 ? c0.x : j == 1 ? c0.y : j == 2 ? c0.z : c0.w, lo);
-            e2m1x8_to_f16x2x4(j == 0 ? c1.x : j == 1 ? c1.y : j == 2 ? c1.z : c1.w, hi);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              lo[e] = hmul2(lo[e], sc[m][0][j >> 1]);
-              hi[e] = hmul2(hi[e], sc[m][1][j >> 1]);
-            }
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(acc[m][n], a0, b[n].x, b[n].y);
-              mma_f16(acc[m][n], a1, b[n].z, b[n].w);
-            }
-          }
+        for (int h = 0; h < 2; ++h) {
+          code[h] += kBatch * (kPiece / 2);
+          scale[h] += kBatch * (kPiece / 16);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 mul = *reinterpret_cast<const float2*>(s_mul + local * kTokens + 8 * n + 2 * t);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            tot[m][n][0] = fmaf(acc[m][n][0], mul.x, tot[m][n][0]);
-            tot[m][n][1] = fmaf(acc[m][n][1], mul.y, tot[m][n][1]);
-            tot[m][n][2] = fmaf(acc[m][n][2], mul.x, tot[m][n][2]);
-            tot[m][n][3] = fmaf(acc[m][n][3], mul.y, tot[m][n][3]);
-          }
-        }
+        x += kBatch * NT * 4 * ru;
+        m += kBatch * tok_p;
       }
-      fetch(step + kDepth, buf[i]);
+#pragma unroll 1
+      for (; p < n; ++p) {
+        Weights w;
+        const bool here = static_cast<int64_t>(lo + p) * kPiece + 32 * t < a.k;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w.code[h] = make_uint4(0, 0, 0, 0);
+          w.scale[h] = 0;
+          if (here) {
+            w.code[h] = load_stream(code[h]);
+            w.scale[h] = load_two(scale[h]);
+          }
+          code[h] += kPiece / 2;
+          scale[h] += kPiece / 16;
+        }
+        add_piece(w, x, m);
+        x += NT * 4 * ru;
+        m += tok_p;
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = 8 * i + 2 * t + (e & 1), at = r + 8 * (e >> 1);
+          if (tok < tok_p && at < rows_cta) s_sum[(w_k * tok_p + tok) * pitch + at] += tot[i][e];
+        }
     }
   }
 
   // ---- sums of the warps along k, then of the cluster's CTAs, each in its order
-  __syncthreads();
-  float* const s_sum = reinterpret_cast<float*>(smem);  // [w_k][token][row]
-  const int pitch = rows_cta + 4;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s_sum[(w_k * kTokens + 8 * n + 2 * t + (e & 1)) * pitch + 16 * (MT * w_row + m) + g + 8 * (e >> 1)] = tot[m][n][e];
   if (a.splits > 1)
     cluster_sync_all();
   else
     __syncthreads();
   const float factor = a.weight_scale != nullptr ? a.weight_scale[grp] : 1.f;
-  const int each = rows_cta / a.splits;  // rows that this CTA finishes, and the remainder in the last
-  const int r_lo = split * each, r_n = split + 1 == a.splits ? rows_cta - r_lo : each;
+  const int each = (rows_cta + a.splits - 1) / a.splits;  // rows that a CTA finishes
+  const int r_lo = min(split * each, rows_cta), r_n = min(each, rows_cta - r_lo);
   for (int i = threadIdx.x; i < r_n * toks; i += kThreads) {
     const int tok = i / r_n, r = r_lo + (i - tok * r_n);
-    if (row0 + r >= a.n) continue;
     float y = 0.f;
-    for (int c = 0; c < a.splits; ++c) {
-      for (int k = 0; k < wk; ++k) {
-        const float* p = s_sum + (k * kTokens + tok) * pitch + r;
-        y += a.splits > 1 ? cluster_read(p, c) : *p;
+    for (int k = 0; k < wk; ++k) {
+      const float* p = s_sum + (k * tok_p + tok) * pitch + r;
+      if (a.splits > 1) {
+        float v[kMaxSplits];
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) v[c] = c < a.splits ? cluster_read(p, c) : 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c) y += v[c];
+      } else {
+        y += *p;
       }
     }
     y *= factor;
@@ -283,66 +371,101 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArg
   if (a.splits > 1) cluster_sync_all();  // nobody leaves while its sums are read
 }
 
-template <int MT, int NT, bool kCodes>
+template <int NT, bool kCodes>
 cudaError_t launch(const MatvecArgs& a, cudaStream_t stream) {
-  const void* kernel = reinterpret_cast<const void*>(fp4_matvec_kernel<MT, NT, kCodes>);
+  const void* kernel = reinterpret_cast<const void*>(fp4_matvec_kernel<NT, kCodes>);
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = set_smem_limit_once(kernel, smem_bytes(MT, NT), &configured);
+  cudaError_t e = set_smem_limit_once(kernel, kSmemBytes, &configured);
   if (e != cudaSuccess) return e;
-  const int64_t rows = 16LL * MT * a.row_warps;
-  const int64_t blocks = (a.n + rows - 1) / rows * a.splits;
+  const int64_t blocks = (a.n + a.rows - 1) / a.rows * a.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.groups),
                      static_cast<unsigned>((a.tokens + 8 * NT - 1) / (8 * NT)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(MT, NT);
+  cfg.blockDim = dim3(32 << warp_bits(NT));
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(a.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
   MatvecArgs args = a;
   void* params[] = {&args};
   e = cudaLaunchKernelExC(&cfg, kernel, params);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// How the rows and k are split: modelled cycles of an SM whose CTAs are resident at
+// once.  The longer of its pieces (`cycles` each with every warp busy) and of one
+// warp's batches (`wait` each), the rounds in which the tokens are laid out, and
+// what a cluster costs.  Measured (the chosen one first; row warps, splits, CTAs an
+// SM): one token x 12288 x 6144 14.3 us with 2, 1, 3, then 15.3 (1, 1, 3), 17.2 (2, 2,
+// 3), 17.4 (4, 1, 3), 18.4 (1, 1, 2); 16 tokens x 8192 x 8192 20.6 with 8, 2, 1, then
+// 21.9 (16, 2, 1), 29.5 (1, 1, 1), 32.4 (16, 4, 1).
+bool plan(MatvecArgs* a, int nt, int tok_p) {
+  const int cycles = nt == 1 ? 64 : nt == 2 ? 100 : 170;
+  const int wait = nt == 1 ? 4000 : nt == 2 ? 5500 : 4500;
+  const int warps = 1 << warp_bits(nt);
+  const int64_t sms = device_sm_count();
+  const int pieces = (a->k + kPiece - 1) / kPiece;
+  const int64_t others = static_cast<int64_t>(a->groups) * ((a->tokens + 8 * nt - 1) / (8 * nt));
+  int64_t best = -1;
+  for (int s = 1; s <= kMaxSplits && s <= pieces; s *= 2)
+    for (int res = resident(nt); res >= 1; --res) {
+      int64_t blocks = sms * res / (s * others);
+      if (blocks < 1) blocks = 1;
+      if (blocks > a->n) blocks = a->n;
+      int64_t rows = (a->n + blocks - 1) / blocks;
+      if (rows > kMaxRows) rows = kMaxRows;
+      const int tiles = static_cast<int>((rows + 15) / 16);
+      const int slice = (pieces + s - 1) / s;
+      const int stage = slice < stage_tasks(nt) / tok_p ? slice : stage_tasks(nt) / tok_p;
+      const int64_t rounds = ((a->n + rows - 1) / rows * s * others + sms * res - 1) / (sms * res);
+      const int stages = (slice + stage - 1) / stage;
+      const int lays = (stage * tok_p + warps * 16 - 1) / (warps * 16) * stages;
+      for (int bits = 0; bits <= warp_bits(nt); ++bits) {
+        const int wr = 1 << bits, wk = warps / wr;
+        const int64_t smem = static_cast<int64_t>(stage) * piece_bytes(nt, tok_p) + sum_bytes(tok_p, wk, rows);
+        if (smem > kSmemBytes / res - (res > 1 ? 1024 : 0)) continue;
+        const int share = (stage + wk - 1) / wk;
+        const int64_t batches = static_cast<int64_t>(stages) * ((tiles + wr - 1) / wr) *
+                                (share / batch(nt) + (share % batch(nt) + 1) / 2);
+        const int64_t work = static_cast<int64_t>(res) * tiles * slice * cycles;
+        const int64_t cost =
+            rounds * ((work > batches * wait ? work : batches * wait) + lays * 4000 + (s > 1 ? 3500 + 500 * s : 0));
+        if (best < 0 || cost < best) {
+          best = cost;
+          a->row_warps_bits = bits;
+          a->slice = slice;
+          a->splits = s;
+          a->rows = static_cast<int>(rows);
+          a->stage = stage;
+          a->smem = static_cast<int>(smem);
+        }
+      }
+    }
+  return best >= 0;
+}
+
 }  // namespace
 
 cudaError_t launch_fp4_matvec(MatvecArgs a, cudaStream_t stream) {
   const int nt = a.tokens <= 8 ? 1 : a.tokens <= 16 ? 2 : 4;
-  const int mt = nt == 2 ? 2 : 1;
-  const int64_t sms = device_sm_count();
-  const int pieces = (a.k + kPiece - 1) / kPiece;
-  const int64_t others = static_cast<int64_t>(a.groups) * ((a.tokens + 8 * nt - 1) / (8 * nt));
-  // Modelled time of the call: CTAs in waves of two a SM, each its pieces' weights and
-  // tokens (in rows) and a start worth 2,000 row pieces.
-  int64_t best = -1;
-  for (int wr = nt == 4 ? 2 : 1; wr <= kWarps; wr *= 2)  // a stage is a whole number of every warp's register pieces
-    for (int s = 1; s <= 8 && s <= pieces; ++s) {
-      const int64_t rows = 16LL * mt * wr;
-      const int64_t ctas = (a.n + rows - 1) / rows * s * others;
-      const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
-      const int wk = kWarps / wr;
-      const int64_t mine = ((pieces + s - 1) / s + wk - 1) / wk * wk;
-      const int64_t cost = waves * (mine * (rows + 8 * nt) + 2000 + (s > 1 ? 500 : 0));
-      if (best < 0 || cost < best) {
-        best = cost;
-        a.row_warps = wr;
-        a.splits = s;
-      }
-    }
+  int tok_p = 8 * nt;
+  while (nt == 1 && tok_p / 2 >= a.tokens) tok_p /= 2;
+  if (!plan(&a, nt, tok_p)) return cudaErrorInvalidConfiguration;
   if (a.x_codes) {
-    if (nt == 1) return launch<1, 1, true>(a, stream);
-    if (nt == 2) return launch<2, 2, true>(a, stream);
-    return launch<1, 4, true>(a, stream);
+    if (nt == 1) return launch<1, true>(a, stream);
+    if (nt == 2) return launch<2, true>(a, stream);
+    return launch<4, true>(a, stream);
   }
-  if (nt == 1) return launch<1, 1, false>(a, stream);
-  if (nt == 2) return launch<2, 2, false>(a, stream);
-  return launch<1, 4, false>(a, stream);
+  if (nt == 1) return launch<1, false>(a, stream);
+  if (nt == 2) return launch<2, false>(a, stream);
+  return launch<4, false>(a, stream);
 }
 
 }  // namespace mla

@@ -256,7 +256,7 @@ struct MatvecArgs {
   bool out_float;
   int64_t out_token, out_group;
   // set by the launch
-  int row_warps, splits;
+  int row_warps_bits, splits, rows, slice, stage, smem;
 };
 cudaError_t launch_fp4_matvec(MatvecArgs a, cudaStream_t stream);
 
