@@ -207,6 +207,7 @@ struct PromptArgs {
   float* lse;  // [q_tokens, heads] or null
   // set by the launch from the plan
   int group, splits, places;
+  bool out_wide;  // rows of out begin and end at multiples of 32 bytes
   float* part_o;
   float* part_lse;
   unsigned int* fault_word;

@@ -11,15 +11,18 @@
 // Rows.  The G query heads of a key head share its keys: a tile is 128 / G tokens
 // x G heads, so a few tokens of many heads fill it as well as many tokens of one.
 //
-// Work split.  One CTA has two tiles of one sequence and key head and walks
-// (a slice of) their keys; the tensor core works on one tile while the other's
-// softmax runs.  Tiles lie in tensor memory: S 2 x 128 columns, O 2 x 128; P
-// overlays S as the A operand of its product.  Warp 0 issues the products, warp
-// 1 the copies, warps 2 and 3 look through the values that some row must not see,
-// and two groups of four warps have a tile's softmax, a thread a row: maximum and
-// sum stay in registers.  Products of one issuing thread complete in order, so a
-// full S says that the product before it, which read P and V, is done too.
-// Slices' partial outputs are joined by their LSEs in a second kernel.
+// Work split.  A unit is two tiles of one sequence and key head and (a slice of)
+// their keys; the tensor core works on one tile while the other's softmax runs.
+// Tiles lie in tensor memory: S 2 x 128 columns, O 2 x 128; P overlays S as the A
+// operand of its product.  A CTA an SM takes units until none is left: the grid
+// has one CTA a unit, and a running one cancels the next that has not started and
+// takes its place, so the next unit's copies and first products overlap the end of
+// this one's.  Warp 0 issues the products, warp 1 the copies, warp 2 looks through
+// the values that some row must not see, warp 3 finds the units, and two groups of
+// four warps have a tile's softmax, a thread a row: maximum and sum stay in
+// registers.  Products of one issuing thread complete in order, so a full S says
+// that the product before it, which read P and V, is done too.  Slices' partial
+// outputs are joined by their LSEs in a second kernel.
 //
 // Values that a row must not see.  A weight of 0 does not keep an infinity or
 // NaN out of a product.  Where some row's mask cuts a tile of keys, its values are
@@ -42,10 +45,11 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 128;    // rows of a tile, and keys of one
-constexpr int kMmaWarp = 0, kCopyWarp = 1, kCleanWarp = 2, kFirstSoftmax = 4;
+constexpr int kMmaWarp = 0, kCopyWarp = 1, kUnitWarp = 3, kFirstSoftmax = 4;  // warp 2: the values
 constexpr int kThreads = 12 * 32;
 constexpr int kChunkBytes = kTile * 128;  // 128 rows of 64 values
 constexpr int kItems = 16;                // barriers of copied tiles (keys and values in turn)
+constexpr int kUnits = 2;                 // units that are known: one in work, one ahead
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kCtlBytes = 1024;
 constexpr uint32_t kSCol = 0, kOCol = 256, kTmemCols = 512;
@@ -56,16 +60,34 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaskedTiles = 3;
 // Registers of the 128 issuing and searching threads, and of the 256 of the softmax:
 // together what 384 threads are launched with.
-constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
+constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
 static_assert(128 * kFewRegs + 256 * kManyRegs == kThreads * kLaunchRegs, "registers");
 
+// Two tiles of a sequence's query tokens, one key head, tiles of keys [begin, begin +
+// count[s]) for tile s.
+struct Unit {
+  int q0, nq;  // the sequence's first query token and their number
+  int k0, nk;
+  int tok;     // first token of tile 0 within the sequence; tile 1's follow
+  int head;    // key head
+  int split;
+  int begin;
+  int count[2];
+  int first_masked;  // tiles of keys from this one on are not seen in full by some row
+  int last;          // nothing comes any more
+};
 struct Ctl {
-  uint64_t q_full[2], full[kItems], free_[kItems], s_full[2], p_full[2], o_full[2], done;
-  uint64_t masked_full[kMaskedTiles], clean[kMaskedTiles];  // values of masked tiles: copied, searched
+  uint64_t unit_full[kUnits], unit_free[kUnits];
+  uint64_t q_full[2], q_free[2];
+  uint64_t full[kItems], free_[kItems];  // copied tiles
+  uint64_t ready[kItems / 2];            // values that have been searched
+  uint64_t s_full[2], p_full[2][2], o_full[2], done, canceled, wanted;
+  uint4 answer;  // to the request for another unit
+  Unit unit[kUnits];
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t bad[kMaskedTiles][kTile / 32];  // keys of the masked tiles that held an infinity or NaN
-  int any_bad;
+  uint32_t bad[kUnits][kMaskedTiles][kTile / 32];  // keys of the masked tiles that held an infinity or NaN
+  int any_bad[kUnits];
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
@@ -79,8 +101,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
       "%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -90,6 +111,28 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
         "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// All loads of this thread have come; r's first use stays behind it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+      :
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -182,17 +225,75 @@ __device__ __forceinline__ bool wait_bar_warp(Ctl& sm, uint64_t* bar, uint32_t p
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// One CTA's part: two tiles of a sequence's query tokens, one key head, tiles of
-// keys [begin, begin + count[s]) for tile s.
-struct Unit {
-  int q0, nq;        // the sequence's first query token and their number
-  int k0, nk;
-  int tok[2];        // first token of either tile within the sequence
-  int head;          // key head
-  int begin;
-  int count[2];
-  int split;
-};
+// Asks for the next CTA that has not started, to be canceled; the answer comes to
+// shared memory.
+__device__ __forceinline__ void request_unit(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Its number, or -1: there is none.
+__device__ __forceinline__ int requested_unit(const void* answer) {
+  int id;
+  asm volatile(
+      "{ .reg .b128 r; .reg .pred p; .reg .b32 x, y, z, w;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 x, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {x, y, z, w}, r;\n\t"
+      "mov.b32 %0, x; }"
+      : "=r"(id)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return id;
+}
+
+// Keys that token i of the unit's sequence sees: the first so many.
+__device__ __forceinline__ int visible(const PromptArgs& a, int nq, int nk, int i) {
+  return a.causal ? min(max(nk - nq + i + 1, 0), nk) : nk;
+}
+// Unit `id`, found by a whole warp; false if it is empty.  Sequence b's pairs of tiles
+// have the places from q_start[b] / tokens + b on: as many as there are places before
+// sequence b + 1's, or fewer.
+__device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane, Unit& u) {
+  const int per = kTile / a.group;  // tokens of a tile
+  u.split = id % a.splits;
+  const int rest = id / a.splits;
+  u.head = rest % a.kv_heads;
+  const int place = a.places - 1 - rest / a.kv_heads;  // the longest rows of a sequence first
+  auto first_place = [&](int b) { return min(max(a.q_start[b], 0), a.q_tokens) / (2 * per) + b; };
+  int lo = -1, hi = a.batch;  // the last b in [lo, hi) whose first place is not behind this one
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int b = lo + (lane + 1) * step;
+    const uint32_t before = __ballot_sync(0xFFFFFFFFu, b < hi && first_place(b) <= place);
+    lo += __popc(before) * step;
+    hi = min(hi, lo + step);
+  }
+  if (lo < 0) return false;
+  u.q0 = min(max(a.q_start[lo], 0), a.q_tokens);
+  u.nq = max(0, min(max(a.q_start[lo + 1], 0), a.q_tokens) - u.q0);
+  u.k0 = min(max(a.kv_start[lo], 0), a.kv_tokens);
+  u.nk = max(0, min(max(a.kv_start[lo + 1], 0), a.kv_tokens) - u.k0);
+  u.tok = (place - (u.q0 / (2 * per) + lo)) * 2 * per;
+  u.last = 0;
+  if (u.tok < 0 || u.tok >= u.nq) return false;
+  int n[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int t = u.tok + s * per;
+    n[s] = t < u.nq ? (visible(a, u.nq, u.nk, min(t + per, u.nq) - 1) + kTile - 1) / kTile : 0;
+  }
+  const int64_t all = max(n[0], n[1]);
+  u.begin = static_cast<int>(all * u.split / a.splits);
+  const int end = static_cast<int>(all * (u.split + 1) / a.splits);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) u.count[s] = max(0, min(end, n[s]) - u.begin);
+  u.first_masked = visible(a, u.nq, u.nk, u.tok) / kTile;
+  return true;
+}
 
 template <int KC, int VC>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -208,73 +309,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned int* fw = args.fault_word;
 
+  if (threadIdx.x == 32 * kCopyWarp)
+    for (const CUtensorMap* m : {&q_map, &k_map, &v_map})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- which tiles.  Sequence b's pairs of tiles have the places from q_start[b] /
-  // tokens + b on: as many as there are places before sequence b + 1's, or fewer.
-  const int per = kTile / args.group;  // tokens of a tile
-  Unit u;
-  u.split = blockIdx.x % args.splits;
-  const int rest = blockIdx.x / args.splits;
-  u.head = rest % args.kv_heads;
-  const int place = args.places - 1 - rest / args.kv_heads;  // the longest rows of a sequence first
-  int seq = -1;
-  for (int b0 = 0; b0 < args.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    bool before = false;
-    if (b < args.batch) {
-      const int at = min(max(args.q_start[b], 0), args.q_tokens);
-      before = at / (2 * per) + b <= place;
-    }
-    seq += __syncthreads_count(before);
-  }
-  if (seq < 0) return;
-  u.q0 = min(max(args.q_start[seq], 0), args.q_tokens);
-  u.nq = max(0, min(max(args.q_start[seq + 1], 0), args.q_tokens) - u.q0);
-  u.k0 = min(max(args.kv_start[seq], 0), args.kv_tokens);
-  u.nk = max(0, min(max(args.kv_start[seq + 1], 0), args.kv_tokens) - u.k0);
-  u.tok[0] = (place - (u.q0 / (2 * per) + seq)) * 2 * per;
-  u.tok[1] = u.tok[0] + per;
-  if (u.tok[0] >= u.nq) return;
-  // keys that token i of the sequence sees: the first limit(i)
-  auto limit = [&](int i) { return args.causal ? min(max(u.nk - u.nq + i + 1, 0), u.nk) : u.nk; };
-  {
-    int n[2];
-    for (int s = 0; s < 2; ++s)
-      n[s] = u.tok[s] < u.nq ? (limit(min(u.tok[s] + per, u.nq) - 1) + kTile - 1) / kTile : 0;
-    const int64_t all = max(n[0], n[1]);
-    u.begin = static_cast<int>(all * u.split / args.splits);
-    const int end = static_cast<int>(all * (u.split + 1) / args.splits);
-    for (int s = 0; s < 2; ++s) u.count[s] = max(0, min(end, n[s]) - u.begin);
-  }
-  const int n_tiles = max(u.count[0], u.count[1]);
-  // tiles of keys that some row does not see in full, from this one on
-  const int first_masked = limit(u.tok[0]) / kTile;
-  const int rows = per * args.group;
-
+  const int per = kTile / args.group, rows = per * args.group;  // tokens and rows of a tile
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&sm.unit_full[i], 1);
+      mbar_init(&sm.unit_free[i], 3 + 8);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_free[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_full[i][0], 4);
+      mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.free_[i], 1);
     }
-    for (int i = 0; i < kMaskedTiles; ++i) {
-      mbar_init(&sm.masked_full[i], 1);
-      mbar_init(&sm.clean[i], 2);
-    }
+    for (int i = 0; i < kItems / 2; ++i) mbar_init(&sm.ready[i], 1);
     mbar_init(&sm.done, 1);
+    mbar_init(&sm.canceled, 1);
+    mbar_init(&sm.wanted, 1);
     sm.abort_flag = 0;
-    sm.any_bad = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x >= 32 && threadIdx.x < 32 + kMaskedTiles * 4)
-    sm.bad[(threadIdx.x - 32) >> 2][threadIdx.x & 3] = 0;
   if (warp == kMmaWarp) {
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
@@ -287,59 +352,107 @@ __global__ void __launch_bounds__(kThreads, 1)
   tcgen05_fence_after();
   // all 512 tensor-memory columns were allocated: they start at column 0
 
-  // Copied tiles in turn: item 2 j has the keys of tile j, item 2 j + 1 the values.
-  // Their chunks follow one another around the ring.
-  auto chunk_of = [](int item) { return (item >> 1) * kPairChunks + (item & 1) * KC; };
-  // The values of masked tiles, at most the last three of a sequence, have barriers
-  // of their own, which the searching warps can wait for from the start.
-  auto masked = [&](int j) { return u.begin + j - first_masked; };  // which one tile j is, negative: none
-  auto full_bar = [&](int item) {
-    return (item & 1) && masked(item >> 1) >= 0 ? &sm.masked_full[masked(item >> 1)] : &sm.full[item % kItems];
-  };
-  auto full_parity = [&](int item) {
-    return (item & 1) && masked(item >> 1) >= 0 ? 0u : static_cast<uint32_t>(item / kItems) & 1u;
-  };
-  auto item_full = [&](int item) { return wait_bar(sm, full_bar(item), full_parity(item), fw); };
+  // Copied tiles in turn, over all units: an even item has the keys of a tile, the next
+  // one its values.  Their chunks follow one another around the ring.
+  auto parity = [](int item) { return static_cast<uint32_t>(item / kItems) & 1u; };
+  auto unit_parity = [](int i) { return static_cast<uint32_t>(i / kUnits) & 1u; };
 
   if (warp < kFirstSoftmax) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-    if (warp == kCopyWarp) {
-      // ---------------------------------------------------------- copies
-      int issued = 0;  // items whose copy was started
-      bool q_issued[2] = {false, false};
-      if (elect_one()) {
-        auto copy_q = [&](int s) {
-          mbar_expect_tx(&sm.q_full[s], static_cast<uint32_t>(KC * rows * 128));
-          q_issued[s] = true;
-          for (int c = 0; c < KC; ++c)
-            tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, u.head * args.group, u.q0 + u.tok[s],
-                        &sm.q_full[s]);
-        };
-        int freed = 0;  // items known to be free again
-        bool ok = true;
-        for (int i = 0; i < 2 * n_tiles && ok; ++i) {
-          const int chunks = (i & 1) ? VC : KC;
-          const int first = chunk_of(i);
-          // the items before this one whose places it takes
-          while (ok && chunk_of(freed) < first + chunks - kRing) {
-            ok = wait_bar(sm, &sm.free_[freed % kItems], static_cast<uint32_t>(freed / kItems) & 1u, fw);
-            ++freed;
+    if (warp == kUnitWarp) {
+      // ---------------------------------------------------------- units
+      int id = blockIdx.x, n = 0;
+      bool ok = true;
+      for (uint32_t asked = 0, found = 0; ok && id >= 0; ++asked) {
+        Unit u;
+        if (find_unit(args, id, lane, u)) {
+          if (n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
+          if (ok && lane == 0) {
+            sm.unit[n % kUnits] = u;
+            sm.any_bad[n % kUnits] = 0;
+            for (int i = 0; i < kMaskedTiles * (kTile / 32); ++i) sm.bad[n % kUnits][0][i] = 0;
+            mbar_arrive(&sm.unit_full[n % kUnits]);
           }
+          ++n;
+          // The next one is asked for when this one's last copies have been started, two
+          // or three tiles before its end: a long unit's successor is for whoever is free
+          // first (asked for at once, 6000 tokens x 16 heads took 172 us).
+          if (ok) ok = wait_bar_warp(sm, &sm.wanted, found & 1u, fw);
+          ++found;
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(&sm.canceled, 16);
+          request_unit(&sm.answer, &sm.canceled);
+        }
+        __syncwarp();
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sm.canceled, asked & 1u, fw, kFaultPromptWait));
+        id = requested_unit(&sm.answer);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (ok && n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
+      if (ok && lane == 0) {
+        sm.unit[n % kUnits].last = 1;
+        mbar_arrive(&sm.unit_full[n % kUnits]);
+      }
+      __syncwarp();
+    } else if (warp == kCopyWarp) {
+      // ---------------------------------------------------------- copies
+      if (elect_one()) {
+        int issued = 0, freed = 0;                  // items
+        int at = 0, at_freed = 0;                   // first chunk of the next item, and of the next that will be free
+        uint32_t q_uses[2] = {0, 0};
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+          ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
           if (!ok) break;
-          if (i == 0 && u.count[0] > 0) copy_q(0);
-          uint64_t* const bar = full_bar(i);
-          mbar_expect_tx(bar, static_cast<uint32_t>(chunks * kChunkBytes));
-          for (int c = 0; c < chunks; ++c)
-            tma_load_3d(s_ring + (first + c) % kRing * kChunkBytes, (i & 1) ? &v_map : &k_map, 64 * c, u.head,
-                        u.k0 + (u.begin + (i >> 1)) * kTile, bar);
-          issued = i + 1;
-          if (i == 0 && u.count[1] > 0) copy_q(1);
+          const Unit& u = sm.unit[n % kUnits];
+          if (u.last) break;
+          const int q_row = u.q0 + u.tok, k_row = u.k0 + u.begin * kTile, head = u.head;
+          const int counts[2] = {u.count[0], u.count[1]};
+          mbar_arrive(&sm.unit_free[n % kUnits]);
+          const int items = 2 * max(counts[0], counts[1]);
+          auto copy_q = [&](int s) {
+            if (q_uses[s] > 0) ok = wait_bar(sm, &sm.q_free[s], (q_uses[s] - 1) & 1u, fw);
+            if (!ok) return;
+            mbar_expect_tx(&sm.q_full[s], static_cast<uint32_t>(KC * rows * 128));
+            ++q_uses[s];
+            for (int c = 0; c < KC; ++c)
+              tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, head * args.group, q_row + s * per, &sm.q_full[s]);
+          };
+          for (int i = 0; i < items && ok; ++i) {
+            const int chunks = (i & 1) ? VC : KC;
+            // the items before this one whose places it takes
+            while (ok && at_freed < at + chunks - kRing) {
+              ok = wait_bar(sm, &sm.free_[freed % kItems], parity(freed), fw);
+              at_freed += (freed & 1) ? VC : KC;
+              ++freed;
+            }
+            if (!ok) break;
+            uint64_t* const bar = &sm.full[issued % kItems];
+            mbar_expect_tx(bar, static_cast<uint32_t>(chunks * kChunkBytes));
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(s_ring + (at + c) % kRing * kChunkBytes, (i & 1) ? &v_map : &k_map, 64 * c, head,
+                          k_row + (i >> 1) * kTile, bar);
+            ++issued;
+            at += chunks;
+            if (at >= 2 * kRing && at_freed >= kRing) {  // both count from the same round of the ring
+              at -= kRing;
+              at_freed -= kRing;
+            }
+            if (i == 0) {
+              if (counts[0] > 0) copy_q(0);
+              if (ok && counts[1] > 0) copy_q(1);
+            }
+          }
+          if (ok) mbar_arrive(&sm.wanted);
         }
         // no copy may be in flight when the CTA leaves
         for (int s = 0; s < 2; ++s)
-          if (q_issued[s]) mbar_wait_bounded(&sm.q_full[s], 0u, fw, kFaultPromptWait);
+          if (q_uses[s] > 0) mbar_wait_bounded(&sm.q_full[s], (q_uses[s] - 1) & 1u, fw, kFaultPromptWait);
         for (int i = max(0, issued - kItems); i < issued; ++i)
-          mbar_wait_bounded(full_bar(i), full_parity(i), fw, kFaultPromptWait);
+          mbar_wait_bounded(&sm.full[i % kItems], parity(i), fw, kFaultPromptWait);
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -349,67 +462,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         const uint64_t q_desc = umma_desc_sw128(smem_u32(s_q));
         const uint32_t ring = smem_u32(s_ring);
-        auto scores = [&](int s, int j) {  // S of tile s and keys j
-          const int first = chunk_of(2 * j);
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint64_t k_desc = umma_desc_sw128(ring + (first + c) % kRing * kChunkBytes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              umma_ss(kSCol + kTile * s, q_desc + (((s * KC + c) * kChunkBytes + 32 * i) >> 4), k_desc + (32 * i >> 4),
-                      idesc_s, c > 0 || i > 0);
-          }
-          umma_commit(&sm.s_full[s]);
-        };
+        int item = 0, at = 0;  // the unit's first item and its first chunk's place in the ring
+        uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
         bool ok = true;
-        if (n_tiles > 0) {
-          ok = item_full(0);
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (u.count[s] == 0) continue;
-            ok = wait_bar(sm, &sm.q_full[s], 0u, fw);
-            if (!ok) break;
-            tcgen05_fence_after();
-            scores(s, 0);
-          }
-          umma_commit(&sm.free_[0]);
-        }
 #pragma unroll 1
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          ok = item_full(2 * j + 1);
-          if (ok && masked(j) >= 0) ok = wait_bar(sm, &sm.clean[masked(j)], 0u, fw);
-          if (ok && j + 1 < n_tiles) ok = item_full(2 * j + 2);
-          const int v0 = chunk_of(2 * j + 1);
+        for (int n = 0; ok; ++n) {
+          ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
+          if (!ok || sm.unit[n % kUnits].last) break;
+          const int count[2] = {sm.unit[n % kUnits].count[0], sm.unit[n % kUnits].count[1]};
+          mbar_arrive(&sm.unit_free[n % kUnits]);
+          const int n_tiles = max(count[0], count[1]);
+          if (n_tiles == 0) continue;
+          auto scores = [&](int s, int j, int k_at) {  // S of tile s and keys j, which begin at chunk k_at
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+              const int chunk = k_at + c >= kRing ? k_at + c - kRing : k_at + c;
+              const uint64_t k_desc = umma_desc_sw128(ring + chunk * kChunkBytes);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_ss(kSCol + kTile * s, q_desc + (((s * KC + c) * kChunkBytes + 32 * i) >> 4), k_desc + (32 * i >> 4),
+                        idesc_s, c > 0 || i > 0);
+            }
+            umma_commit(&sm.s_full[s]);
+            if (j + 1 == count[s]) umma_commit(&sm.q_free[s]);
+          };
+          ok = wait_bar(sm, &sm.full[item % kItems], parity(item), fw);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (ok && j < u.count[s]) {
-              ok = wait_bar(sm, &sm.p_full[s], static_cast<uint32_t>(j) & 1u, fw);
-              if (!ok) break;
-              tcgen05_fence_after();
-              // the two chunks of a value tile may lie at the ring's two ends
-              uint32_t at[VC];
+            if (!ok || count[s] == 0) continue;
+            ok = wait_bar(sm, &sm.q_full[s], q_uses[s] & 1u, fw);
+            ++q_uses[s];
+            if (!ok) continue;
+            tcgen05_fence_after();
+            scores(s, 0, at);
+          }
+          umma_commit(&sm.free_[item % kItems]);
+#pragma unroll 1
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            const int v_item = item + 1, k_item = item + 2;
+            int v_at = at + KC, k_at = at + kPairChunks;
+            v_at = v_at >= kRing ? v_at - kRing : v_at;
+            k_at = k_at >= kRing ? k_at - kRing : k_at;
+            ok = wait_bar(sm, &sm.ready[v_item / 2 % (kItems / 2)], parity(v_item), fw);
+            if (ok && j + 1 < n_tiles) ok = wait_bar(sm, &sm.full[k_item % kItems], parity(k_item), fw);
 #pragma unroll
-              for (int c = 0; c < VC; ++c) at[c] = ring + (v0 + c) % kRing * kChunkBytes;
-              if (VC == 1 || at[VC - 1] == at[0] + kChunkBytes) {
-                const uint64_t v_desc = desc_values(at[0]);
+            for (int s = 0; s < 2; ++s) {
+              if (ok && j < count[s]) {
+                // the product of the first half of the keys runs while the other's weights
+                // are computed
 #pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                  umma_ts(kOCol + kTile * s, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, j > 0 || i > 0);
-              } else {
+                for (int half = 0; half < 2; ++half) {
+                  if (ok) ok = wait_bar(sm, &sm.p_full[s][half], p_uses[s] & 1u, fw);
+                  if (!ok) continue;
+                  tcgen05_fence_after();
+                  // the two chunks of a value tile may lie at the ring's two ends
+                  const uint32_t v0 = ring + v_at * kChunkBytes;
+                  if (VC == 1 || v_at + 1 < kRing) {
+                    const uint64_t v_desc = desc_values(v0);
 #pragma unroll
-                for (int c = 0; c < VC; ++c) {
-                  const uint64_t v_desc = desc_values(at[c]);
+                    for (int i = 4 * half; i < 4 * half + 4; ++i)
+                      umma_ts(kOCol + kTile * s, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, j > 0 || i > 0);
+                  } else {
 #pragma unroll
-                  for (int i = 0; i < kTile / 16; ++i)
-                    umma_ts(kOCol + kTile * s + 64 * c, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4),
-                            bf16_idesc(64, false, true), j > 0 || i > 0);
+                    for (int c = 0; c < VC; ++c) {
+                      const uint64_t v_desc = desc_values(c == 0 ? v0 : ring);
+#pragma unroll
+                      for (int i = 4 * half; i < 4 * half + 4; ++i)
+                        umma_ts(kOCol + kTile * s + 64 * c, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4),
+                                bf16_idesc(64, false, true), j > 0 || i > 0);
+                    }
+                  }
+                }
+                ++p_uses[s];
+                if (ok) {
+                  if (j + 1 == count[s]) umma_commit(&sm.o_full[s]);
                 }
               }
-              if (j + 1 == u.count[s]) umma_commit(&sm.o_full[s]);
+              if (s == 1) umma_commit(&sm.free_[v_item % kItems]);
+              if (ok && j + 1 < count[s]) scores(s, j + 1, k_at);
             }
-            if (s == 1) umma_commit(&sm.free_[(2 * j + 1) % kItems]);
-            if (ok && j + 1 < u.count[s]) scores(s, j + 1);
+            if (j + 1 < n_tiles) umma_commit(&sm.free_[k_item % kItems]);
+            item += 2;
+            at = k_at;
           }
-          if (j + 1 < n_tiles) umma_commit(&sm.free_[(2 * j + 2) % kItems]);
         }
         umma_commit(&sm.done);
         mbar_wait_bounded(&sm.done, 0u, fw, kFaultPromptWait);
@@ -417,41 +552,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- values that are no numbers
-      const int half = warp - kCleanWarp;  // keys 64 half ..
-      for (int j = max(0, first_masked - u.begin); j < n_tiles; ++j) {
-        const int item = 2 * j + 1;
-        if (!wait_bar_warp(sm, full_bar(item), 0u, fw)) break;
+      int item = 1, at = KC;  // the next values and the place of their first chunk in the ring
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        ok = wait_bar_warp(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
+        if (!ok || sm.unit[n % kUnits].last) break;
+        const Unit& u = sm.unit[n % kUnits];
+        const int n_tiles = max(u.count[0], u.count[1]);
+        const int masked0 = u.first_masked - u.begin;  // tiles from this one on
+        const int seen = visible(args, u.nq, u.nk, u.tok);  // keys before it are seen by all rows
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          ok = wait_bar_warp(sm, &sm.full[item % kItems], parity(item), fw);
+          if (!ok) break;
+          if (j >= masked0) {
 #pragma unroll 1
-        for (int r = 0; r < 2; ++r) {
-          const int key = 64 * half + 32 * r + lane;
-          uint32_t top = 0;  // the largest magnitudes, two at a time
+            for (int r = max(0, seen - (u.begin + j) * kTile) / 32; r < kTile / 32; ++r) {
+              const int key = 32 * r + lane;
+              const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+              __nv_bfloat162 sum[4] = {zero, zero, zero, zero};  // of products with 0: NaN where there is one
 #pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            const uint8_t* row = s_ring + (chunk_of(item) + c) % kRing * kChunkBytes + key * 128;
+              for (int c = 0; c < VC; ++c) {
+                const uint8_t* row = s_ring + (at + c >= kRing ? at + c - kRing : at + c) * kChunkBytes + key * 128;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // in another order in each lane, so that they read different banks
-              const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * ((i + lane) & 7));
-              top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
-                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+                for (int i = 0; i < 8; ++i) {  // in another order in each lane, so that they read different banks
+                  const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * ((i + lane) & 7));
+                  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) sum[k] = __hfma2(x[k], zero, sum[k]);
+                }
+              }
+              const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+              const bool bad = __hisnan(all.x) || __hisnan(all.y);
+              const uint32_t which = __ballot_sync(0xFFFFFFFFu, bad);
+              if (bad) {
+                for (int c = 0; c < VC; ++c) {
+                  uint16_t* row = reinterpret_cast<uint16_t*>(
+                      s_ring + (at + c >= kRing ? at + c - kRing : at + c) * kChunkBytes + key * 128);
+                  for (int i = 0; i < 64; ++i)
+                    if ((row[i] & 0x7F80u) == 0x7F80u) row[i] = 0;
+                }
+              }
+              if (which != 0 && lane == 0) {
+                sm.bad[n % kUnits][j - masked0][r] = which;
+                *reinterpret_cast<volatile int*>(&sm.any_bad[n % kUnits]) = 1;
+              }
             }
+            fence_proxy_async_smem();
           }
-          const bool bad = (top & 0x7FFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
-          const uint32_t which = __ballot_sync(0xFFFFFFFFu, bad);
-          if (bad) {
-            for (int c = 0; c < VC; ++c) {
-              uint16_t* row = reinterpret_cast<uint16_t*>(s_ring + (chunk_of(item) + c) % kRing * kChunkBytes + key * 128);
-              for (int i = 0; i < 64; ++i)
-                if ((row[i] & 0x7F80u) == 0x7F80u) row[i] = 0;
-            }
-          }
-          if (which != 0 && lane == 0) {
-            sm.bad[masked(j)][2 * half + r] = which;
-            *reinterpret_cast<volatile int*>(&sm.any_bad) = 1;
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.ready[item / 2 % (kItems / 2)]);
+          item += 2;
+          at += kPairChunks;
+          at = at >= kRing ? at - kRing : at;
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.clean[masked(j)]);
+        if (lane == 0) mbar_arrive(&sm.unit_free[n % kUnits]);
       }
     }
   } else {
@@ -460,154 +615,190 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = (warp - kFirstSoftmax) >> 2;
     const int quad = warp & 3;
     const int row = 32 * quad + lane;
-    const int tok = u.tok[s] + row / args.group;
-    const int head = u.head * args.group + row % args.group;
-    const bool here = row < rows && tok < u.nq;
-    const int count = u.count[s];
+    const int row_tok = row / args.group, row_head = row - row_tok * args.group;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t s_addr = lanes + kSCol + kTile * s, o_addr = lanes + kOCol + kTile * s;
-    const int lim = here ? limit(tok) : 0;
-    const int tile_full = u.tok[s] < u.nq ? limit(u.tok[s]) / kTile : 0;  // tiles that all rows see in full
     const float sl = args.scale_log2;
     const uint64_t sl2 = pack2(sl, sl);
-    float ref = -INFINITY;  // of the scaled scores, base 2
-    uint64_t l2[2] = {0, 0};
+    uint32_t s_uses = 0, o_uses = 0;
     bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < count; ++j) {
-      ok = wait_bar_warp(sm, &sm.s_full[s], static_cast<uint32_t>(j) & 1u, fw);
-      if (!ok) break;
-      tcgen05_fence_after();
-      uint32_t z[2][64];
-      tmem_ld64(s_addr, z[0]);
-      tmem_ld64(s_addr + 64, z[1]);
-      if (u.begin + j >= tile_full) {
-        const int rel = lim - (u.begin + j) * kTile;
-#pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          if (i >= rel) z[i >> 6][i & 63] = 0xFF800000u;
-      }
-      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int i = 0; i < 64; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m[k] = max3(m[k], __uint_as_float(z[half][i + k]), __uint_as_float(z[half][i + 4 + k]));
-      const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sl;
-      const bool raise = top - ref > kLag;
-      if (__any_sync(0xFFFFFFFFu, raise)) {
-        float alpha = 1.f;
-        if (raise) {
-          alpha = ex2(ref - top);  // 0 while nothing has been seen
-          ref = top;
-        }
-        const uint64_t a2 = pack2(alpha, alpha);
-        l2[0] = fma2(l2[0], a2, 0);
-        l2[1] = fma2(l2[1], a2, 0);
-        if (j > 0) {
+    for (int n = 0; ok; ++n) {
+      ok = wait_bar_warp(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
+      if (!ok || sm.unit[n % kUnits].last) break;
+      const Unit& u = sm.unit[n % kUnits];
+      const int count = s == 0 ? u.count[0] : u.count[1];
+      const int tok0 = u.tok + s * per, tok = tok0 + row_tok;
+      const int head = u.head * args.group + row_head;
+      const bool here = row < rows && tok < u.nq;
+      const int lim = here ? visible(args, u.nq, u.nk, tok) : 0;
+      const int begin = u.begin;
+      const int tile_full = tok0 < u.nq ? visible(args, u.nq, u.nk, tok0) / kTile : 0;  // tiles that all rows see in full
+      float ref = -INFINITY;  // of the scaled scores, base 2
+      uint64_t l2[2] = {0, 0};
 #pragma unroll 1
-          for (int c = 0; c < 64 * VC; c += 32) {
-            uint32_t o[32];
-            tmem_load_32cols(o_addr + c, o);
+      for (int j = 0; j < count; ++j) {
+        ok = wait_bar_warp(sm, &sm.s_full[s], s_uses & 1u, fw);
+        ++s_uses;
+        if (!ok) break;
+        tcgen05_fence_after();
+        uint32_t z[2][64];
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld64(s_addr, z[0]);
+        tmem_wait(z[0]);
+        tmem_ld64(s_addr + 64, z[1]);  // on its way while the first half's maximum is taken
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_addr + c, o);
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) tmem_wait(z[1]);
+          if (begin + j >= tile_full) {
+            const int rel = lim - (begin + j) * kTile - 64 * half;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= rel) z[half][i] = 0xFF800000u;
           }
-        }
-      }
-      const float sub = ref == -INFINITY ? 0.f : -ref;
-      const uint64_t sub2 = pack2(sub, sub);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
+          for (int i = 0; i < 64; i += 8)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x, y;
-          unpack2(fma2(pack2(__uint_as_float(z[half][2 * i]), __uint_as_float(z[half][2 * i + 1])), sl2, sub2), x, y);
-          x = ex2(x);
-          y = ex2(y);
-          l2[i & 1] = add2(l2[i & 1], pack2(x, y));
-          p[i] = bf16x2_rn(x, y);
+            for (int k = 0; k < 4; ++k)
+              m[k] = max3(m[k], __uint_as_float(z[half][i + k]), __uint_as_float(z[half][i + 4 + k]));
         }
-        tmem_st32(s_addr + 32 * half, p);
-      }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[s]);
-    }
-    // ---- output
-    float l;
-    {
-      float x0, x1, x2, x3;
-      unpack2(l2[0], x0, x1);
-      unpack2(l2[1], x2, x3);
-      l = (x0 + x1) + (x2 + x3);
-    }
-    if (ok && count > 0) ok = wait_bar_warp(sm, &sm.o_full[s], 0u, fw);
-    if (ok && u.tok[s] < u.nq) {
-      tcgen05_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t t = u.q0 + tok;
-      const bool direct = args.splits == 1;
-      const float lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
-      const int64_t part = (t * args.heads + head) * args.splits + u.split;
-      if (here) {
-        if (!direct)
-          args.part_lse[part] = lse2;
-        else if (args.lse != nullptr)
-          args.lse[t * args.heads + head] = lse2 * kLn2;
-      }
-      const bool bad = *reinterpret_cast<volatile int*>(&sm.any_bad) != 0;
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sl;
+        const bool raise = top - ref > kLag;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          float alpha = 1.f;
+          if (raise) {
+            alpha = ex2(ref - top);  // 0 while nothing has been seen
+            ref = top;
+          }
+          const uint64_t a2 = pack2(alpha, alpha);
+          l2[0] = fma2(l2[0], a2, 0);
+          l2[1] = fma2(l2[1], a2, 0);
+          if (j > 0) {
 #pragma unroll 1
-      for (int c = 0; c < args.dv; c += 32) {
-        uint32_t o[32];
-        if (count > 0) {
-          tmem_load_32cols(o_addr + c, o);
-        } else {
+            for (int c = 0; c < 64 * VC; c += 32) {
+              uint32_t o[32];
+              tmem_load_32cols(o_addr + c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
-        if (bad) {
-#pragma unroll 1
-          for (int w = 0; w < kMaskedTiles * 4; ++w) {
-            uint32_t keys = sm.bad[w >> 2][w & 3];
-            while (keys != 0) {
-              const int key = (first_masked + (w >> 2)) * kTile + 32 * (w & 3) + __ffs(keys) - 1;
-              keys &= keys - 1;
-              if (key >= lim) break;
-              const uint16_t* v = args.v + (u.k0 + key) * args.v_token + u.head * args.v_head + c;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (c + i >= args.dv) break;
-                const uint32_t x = v[i];
-                if ((x & 0x7F80u) == 0x7F80u) o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_bits_to_f32(x));
-              }
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_addr + c, o);
             }
           }
         }
+        const float sub = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t sub2 = pack2(sub, sub);
+        auto publish = [&](int half) {
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[s][half]);
+        };
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+        for (int part = 0; part < 4; ++part) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = 32 * (part & 1) + 2 * i;
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(z[part >> 1][at]), __uint_as_float(z[part >> 1][at + 1])), sl2, sub2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            l2[i & 1] = add2(l2[i & 1], pack2(x, y));
+            p[i] = bf16x2_rn(x, y);
+          }
+          // the first half is given away a quarter later: its stores are over by then
+          if (part == 2) publish(0);
+          tmem_st16(s_addr + 16 * part, p);
+        }
+        publish(1);
+      }
+      // ---- output
+      float l;
+      {
+        float x0, x1, x2, x3;
+        unpack2(l2[0], x0, x1);
+        unpack2(l2[1], x2, x3);
+        l = (x0 + x1) + (x2 + x3);
+      }
+      if (ok && count > 0) {
+        ok = wait_bar_warp(sm, &sm.o_full[s], o_uses & 1u, fw);
+        ++o_uses;
+      }
+      if (ok && tok0 < u.nq) {
+        tcgen05_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t t = u.q0 + tok;
+        const bool direct = args.splits == 1;
+        const float lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
+        const int64_t part = (t * args.heads + head) * args.splits + u.split;
         if (here) {
-          if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(args.out + t * args.out_token + head * args.out_head + c);
+          if (!direct)
+            args.part_lse[part] = lse2;
+          else if (args.lse != nullptr)
+            args.lse[t * args.heads + head] = lse2 * kLn2;
+        }
+        const bool bad = *reinterpret_cast<volatile int*>(&sm.any_bad[n % kUnits]) != 0;
+#pragma unroll 1
+        for (int c = 0; c < args.dv; c += 32) {
+          uint32_t o[32];
+          if (count > 0) {
+            tmem_load_32cols(o_addr + c, o);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c + 8 * i < args.dv)
-                dst[i] = make_uint4(bf16x2_rn(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
-                                    bf16x2_rn(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
-                                    bf16x2_rn(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
-                                    bf16x2_rn(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
-          } else if (l != 0.f) {
-            uint4* dst = reinterpret_cast<uint4*>(args.part_o + part * args.dv + c);
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (bad) {
+#pragma unroll 1
+            for (int w = 0; w < kMaskedTiles * 4; ++w) {
+              uint32_t keys = sm.bad[n % kUnits][w >> 2][w & 3];
+              while (keys != 0) {
+                const int key = (u.first_masked + (w >> 2)) * kTile + 32 * (w & 3) + __ffs(keys) - 1;
+                keys &= keys - 1;
+                if (key >= lim) break;
+                const uint16_t* v = args.v + (u.k0 + key) * args.v_token + u.head * args.v_head + c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + 4 * i < args.dv) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 32; ++i) {
+                  if (c + i >= args.dv) break;
+                  const uint32_t x = v[i];
+                  if ((x & 0x7F80u) == 0x7F80u) o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_bits_to_f32(x));
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+          if (here) {
+              if (direct) {
+              uint16_t* dst = args.out + t * args.out_token + head * args.out_head + c;
+              uint32_t h[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) h[i] = bf16x2_rn(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+              if (args.out_wide) {  // a whole sector a store: half the time of 16-byte ones
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (c + 16 * i < args.dv)
+                    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * i), "r"(h[8 * i]),
+                                 "r"(h[8 * i + 1]), "r"(h[8 * i + 2]), "r"(h[8 * i + 3]), "r"(h[8 * i + 4]),
+                                 "r"(h[8 * i + 5]), "r"(h[8 * i + 6]), "r"(h[8 * i + 7])
+                                 : "memory");
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (c + 8 * i < args.dv)
+                    *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+              }
+            } else if (l != 0.f) {
+              uint4* dst = reinterpret_cast<uint4*>(args.part_o + part * args.dv + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c + 4 * i < args.dv) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
         }
       }
+      // the tensor memory has been read, by this unit's last loads or its next ones' wait
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_free[n % kUnits]);
     }
   }
 
@@ -692,9 +883,12 @@ cudaError_t launch(PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, co
 
 }  // namespace
 
-// How the keys are split: modelled time = full waves of CTAs, each its tiles of
-// keys and a start worth four, and the joining of the partials.  Lengths are known
-// on the device only: every sequence is taken for an equal share of the tokens.
+// How the keys are split: modelled time in tiles of keys.  Up to a unit an SM, a
+// slice and a start worth three; else the SMs' share of all slices and starts, and
+// a slice at the end, when others have run out.  The partials' joining is a launch
+// worth two tiles and their bytes (a tile takes about 1.7 us, in which memory
+// writes and reads 10 MB).  Lengths are known on the device only: every sequence is
+// taken for an equal share of the tokens.
 PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch, int heads, int kv_heads, int dv) {
   PromptPlan p{};
   const int group = heads / kv_heads;
@@ -704,16 +898,19 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
   const int64_t units = (used < p.places ? used : p.places) * kv_heads;
   const int64_t sms = device_sm_count();
   const int64_t tiles = (kv_tokens / batch + kTile - 1) / kTile;
-  int64_t best = -1;
+  const double rows_mb = static_cast<double>(q_tokens) * heads * (dv + 1) * 8e-6;  // of one slice, written and read
+  double best = -1;
   p.splits = 1;
   for (int64_t n = 1; n <= (tiles > 1 ? tiles : 1) && n <= sms; ++n) {
-    const int64_t waves = (units * n + sms - 1) / sms;
-    const int64_t cost = 8 * waves * ((tiles + n - 1) / n + 4) + (n > 1 ? 24 + 4 * n : 0);
+    const double slice = static_cast<double>((tiles + n - 1) / n);
+    double cost = slice + 3;
+    if (units * n > sms) cost = static_cast<double>(units * (tiles + 3 * n)) / static_cast<double>(sms) + slice;
+    if (n > 1) cost += 2 + rows_mb * static_cast<double>(n) * 0.1;
     if (best < 0 || cost < best) {
       best = cost;
       p.splits = static_cast<int>(n);
     }
-    if (units * n > 4 * sms) break;
+    if (units * n > 8 * sms) break;
   }
   if (p.splits > 1)
     p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 1) * sizeof(float) + 255) / 256 * 256;
@@ -726,6 +923,8 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
   a.splits = plan.splits;
   a.places = static_cast<int>(plan.places);
   a.fault_word = fault_word_ptr();
+  a.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.dv % 16 == 0 && (a.q_tokens == 1 || a.out_token % 16 == 0) &&
+               (a.heads == 1 || a.out_head % 16 == 0);
   *described = true;
   if (a.fault_word == nullptr) return cudaErrorInvalidDevicePointer;
   if (a.splits > 1) {
