@@ -444,7 +444,7 @@ def _on(stream, device: int) -> int:
 def _new(like, shape, dtype, stream) -> torch.Tensor:
     """Memory on `like`'s device whose reuse is ordered behind the stream the call runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype) if dtype is not like.dtype else like.new_empty(shape)
+        return torch.empty(shape, dtype=dtype, device=like.device)  # 1.5 us, like.new_empty 2.4
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):

@@ -53,6 +53,10 @@ __host__ __device__ constexpr int row_units(int nt, int toks) { return (nt > 1 ?
 __host__ __device__ constexpr int piece_bytes(int nt, int toks) {
   return nt * 4 * row_units(nt, toks) * 16 + (toks < 4 ? 16 : 4 * toks);
 }
+// e4m3 tokens stay as they are, [token][128 values a piece, and 16 bytes so that two tokens'
+// 16-byte reads do not meet], with their factors behind.
+constexpr int kRawPad = 16;
+__host__ __device__ constexpr int raw_piece_bytes(int toks) { return toks * (kPiece + 4); }
 // Joined sums: [WK][tokens][rows, and 4 to spread the banks] floats.
 __host__ __device__ constexpr int64_t sum_bytes(int toks, int wk, int64_t rows) { return wk * toks * (rows + 4) * 4; }
 
@@ -89,6 +93,9 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kTokens = 8 * NT;
   constexpr int kBatch = batch(NT);
+  // A piece's registers are loaded again as soon as it has been used up; with 24 warps an
+  // SM (one token tile) that gains nothing.
+  constexpr bool kAhead = NT > 1;
   constexpr int kWarpBits = warp_bits(NT), kThreads = 32 << kWarpBits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -134,89 +141,80 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
   const int tok_p = NT > 1 ? kTokens : 1 << tok_bits;  // tokens with a place
   const int ru = row_units(NT, tok_p);
   uint4* const s_x = reinterpret_cast<uint4*>(smem);
-  float* const s_mul = reinterpret_cast<float*>(smem + a.stage * NT * 4 * ru * 16);
-  float* const s_sum = reinterpret_cast<float*>(smem + a.stage * piece_bytes(NT, tok_p));  // [w_k][token][row]
+  const int raw_pitch = a.stage * kPiece + kRawPad;
+  float* const s_mul = reinterpret_cast<float*>(smem + (kCodes ? tok_p * raw_pitch : a.stage * NT * 4 * ru * 16));  // [piece][token]
+  float* const s_sum = reinterpret_cast<float*>(
+      smem + (kCodes ? a.stage * raw_piece_bytes(tok_p) + tok_p * kRawPad : a.stage * piece_bytes(NT, tok_p)));  // [w_k][token][row]
   const int pitch = a.rows + 4;
   const int u = lane & 15;
   const uint32_t half = lane & 16 ? 0xFFFF0000u : 0x0000FFFFu;  // the halves may go different ways
+  // Tokens that are not there leave what the memory holds: theirs are columns of their
+  // own, which nobody reads.
   auto stage_tokens = [&](int s) {
-    const int lo = stage_lo(s), count = stage_n(s) << tok_bits;
-    constexpr int kAhead = 8;
-    constexpr int kRegs = kCodes ? 2 : 4;
-#pragma unroll 1
-    for (int i0 = threadIdx.x >> 4; i0 < count; i0 += kAhead * (kThreads / 16)) {
-      uint32_t raw[kAhead][kRegs];
-      float raw_mul[kCodes ? kAhead : 1];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * (kThreads / 16);
-        const int tok = i & ((1 << tok_bits) - 1), piece = lo + (i >> tok_bits);
-        const int64_t k0 = static_cast<int64_t>(piece) * kPiece + 8 * u;
-#pragma unroll
-        for (int e = 0; e < kRegs; ++e) raw[j][e] = 0;
-        if constexpr (kCodes) raw_mul[j] = 0.f;
-        if (i < count && tok < toks && k0 < a.k) {
-          const int64_t off = (tok0 + tok) * a.x_token + grp * a.x_group + k0;
-          if constexpr (kCodes) {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + off);
-            raw[j][0] = w.x;
-            raw[j][1] = w.y;
-            raw_mul[j] = a.x_scales[((tok0 + tok) * a.groups + grp) * a.x_scale_groups + (a.x_scale_groups > 1 ? piece : 0)];
-          } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + off);
-            raw[j][0] = w.x;
-            raw[j][1] = w.y;
-            raw[j][2] = w.z;
-            raw[j][3] = w.w;
-          }
+    const int lo = stage_lo(s), n = stage_n(s);
+    if constexpr (kCodes) {
+      for (int i = threadIdx.x; i < n * toks; i += kThreads) {
+        const int tok = i / n, piece = i - tok * n;
+        s_mul[piece * tok_p + tok] =
+            a.x_scales[((tok0 + tok) * a.groups + grp) * a.x_scale_groups + (a.x_scale_groups > 1 ? lo + piece : 0)];
+      }
+      const int chunks = n * (kPiece / 16);
+      for (int tok = warp; tok < toks; tok += kThreads / 32) {
+        const uint8_t* src = static_cast<const uint8_t*>(a.x) + (tok0 + tok) * a.x_token + grp * a.x_group;
+        for (int c = lane; c < chunks; c += 32) {
+          const int64_t k0 = static_cast<int64_t>(lo) * kPiece + 16 * c;
+          const bool in = k0 < a.k;  // zeros behind the end of k
+          cp_async16(smem + tok * raw_pitch + 16 * c, in ? src + k0 : src, in ? 16 : 0);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      const int count = n << tok_bits;
+      constexpr int kLoads = 8;
+#pragma unroll 1
+      for (int i0 = threadIdx.x >> 4; i0 < count; i0 += kLoads * (kThreads / 16)) {
+        uint4 raw[kLoads];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * (kThreads / 16);
-        const int tok = i & ((1 << tok_bits) - 1), slot = i >> tok_bits;
-        if (i >= count) continue;
-        uint32_t h[4];
-        float mul;
-        if constexpr (kCodes) {
-          uint32_t lo2[2], hi2[2];
-          e4m3x4_to_f16x2x2(raw[j][0], lo2);
-          e4m3x4_to_f16x2x2(raw[j][1], hi2);
-          h[0] = lo2[0];
-          h[1] = lo2[1];
-          h[2] = hi2[0];
-          h[3] = hi2[1];
-          mul = raw_mul[j];
-        } else {
-          uint32_t mx = bf16x8_absmax_bits(make_uint4(raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
+        for (int j = 0; j < kLoads; ++j) {
+          const int i = i0 + j * (kThreads / 16);
+          const int tok = i & ((1 << tok_bits) - 1), piece = lo + (i >> tok_bits);
+          const int64_t k0 = static_cast<int64_t>(piece) * kPiece + 8 * u;
+          raw[j] = make_uint4(0, 0, 0, 0);
+          if (i < count && tok < toks && k0 < a.k)
+            raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (tok0 + tok) * a.x_token +
+                                                     grp * a.x_group + k0);
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const int i = i0 + j * (kThreads / 16);
+          const int tok = i & ((1 << tok_bits) - 1), slot = i >> tok_bits;
+          if (i >= count) continue;
+          uint32_t mx = bf16x8_absmax_bits(raw[j]);
 #pragma unroll
           for (int m = 8; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(half, mx, m));
           const int shift = query_shift(mx);
           const float up = pow2f(shift);
-          mul = pow2f(-shift);
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t w = raw[j][e];
-            const __half2 p = __floats2half2_rn(bf16_bits_to_f32(w & 0xFFFFu) * up, bf16_bits_to_f32(w >> 16) * up);
+            const __half2 p = __floats2half2_rn(bf16_bits_to_f32(w[e] & 0xFFFFu) * up, bf16_bits_to_f32(w[e] >> 16) * up);
             h[e] = *reinterpret_cast<const uint32_t*>(&p);
           }
+          s_x[((slot * NT + (tok >> 3)) * 4 + (u & 3)) * ru + (tok & 7) * 4 + (u >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
+          if (u == 0) s_mul[slot * tok_p + tok] = pow2f(-shift);
         }
-        s_x[((slot * NT + (tok >> 3)) * 4 + (u & 3)) * ru + (tok & 7) * 4 + (u >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
-        if (u == 0) s_mul[slot * tok_p + tok] = mul;
       }
     }
   };
-  if (NT > 1 && toks < kTokens) {  // the tokens that are not there are zeros
-    for (int i = threadIdx.x; i < a.stage * piece_bytes(NT, tok_p) / 16; i += kThreads) s_x[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
   for (int i = threadIdx.x; i < wk * tok_p * pitch; i += kThreads) s_sum[i] = 0.f;
   const bool x_here = NT > 1 || g < tok_p;      // else this lane's token (of B) has no place
   const bool y_here = NT > 1 || 2 * t < tok_p;  // and its two tokens of the sums
 
+  const int x_step = kCodes ? kPiece : NT * 4 * ru * 16;  // bytes of a piece's tokens
   float tot[NT][4];
   // One piece: its weights and the tokens of place x (of factors m) into the sums.
-  auto add_piece = [&](const Weights& w, const uint4* x, const float* m) {
+  auto add_piece = [&](const Weights& w, const uint8_t* x, const float* m) {
     float acc[NT][4];
     uint32_t sc[2][2];
 #pragma unroll
@@ -224,12 +222,22 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
       sc[h][0] = e4m3x2_to_f16x2(__byte_perm(w.scale[h], 0, 0x4400));
       sc[h][1] = e4m3x2_to_f16x2(__byte_perm(w.scale[h], 0, 0x4411));
     }
+    uint4 raw[kCodes ? NT : 1];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint4 b[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        b[n] = x[(n * 4 + j) * ru];
+        if constexpr (kCodes) {
+          if (j % 2 == 0) raw[n] = *reinterpret_cast<const uint4*>(x + 8 * n * raw_pitch + 8 * j);
+          uint32_t lo2[2], hi2[2];
+          e4m3x4_to_f16x2x2(j % 2 == 0 ? raw[n].x : raw[n].z, lo2);
+          e4m3x4_to_f16x2x2(j % 2 == 0 ? raw[n].y : raw[n].w, hi2);
+          b[n] = make_uint4(lo2[0], lo2[1], hi2[0], hi2[1]);
+        } else {
+          b[n] = *reinterpret_cast<const uint4*>(x + (n * 4 + j) * ru * 16);
+        }
+        // a token without a place has read another's
         if (NT == 1 && !x_here) b[n] = make_uint4(0, 0, 0, 0);
       }
       const uint4 c0 = w.code[0], c1 = w.code[1];
@@ -282,50 +290,59 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
         code[h] = a.codes + row * code_row + static_cast<int64_t>(lo) * (kPiece / 2) + 16 * t;
         scale[h] = a.scales + row * scale_row + static_cast<int64_t>(lo) * (kPiece / 16) + 2 * t;
       }
-      const uint4* x = s_x + share_lo(st) * (NT * 4 * ru) + (x_here ? lane : 0);
+      const uint8_t* x = smem + (kCodes ? share_lo(st) * kPiece + (x_here ? g : 0) * raw_pitch + 32 * t
+                                        : 16 * (share_lo(st) * (NT * 4 * ru) + (x_here ? lane : 0)));
       const float* m = s_mul + share_lo(st) * tok_p + (y_here ? 2 * t : 0);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) tot[i][e] = 0.f;
       int p = 0;
+      Weights w[kBatch];
+      auto load = [&](int i, int ahead) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[i].code[h] = load_stream(code[h] + (ahead + i) * (kPiece / 2));
+          w[i].scale[h] = load_two(scale[h] + (ahead + i) * (kPiece / 16));
+        }
+      };
+      if (kAhead && whole > 0)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) load(i, 0);
 #pragma unroll 1
       for (; p < whole; p += kBatch) {
-        Weights w[kBatch];
+        if (!kAhead)
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
+          for (int i = 0; i < kBatch; ++i) load(i, 0);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            w[i].code[h] = load_stream(code[h] + i * (kPiece / 2));
-            w[i].scale[h] = load_two(scale[h] + i * (kPiece / 16));
-          }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) add_piece(w[i], x + i * (NT * 4 * ru), m + i * tok_p);
+        for (int i = 0; i < kBatch; ++i) {
+          add_piece(w[i], x + i * x_step, m + i * tok_p);
+          if (kAhead && p + kBatch < whole) load(i, kBatch);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           code[h] += kBatch * (kPiece / 2);
           scale[h] += kBatch * (kPiece / 16);
         }
-        x += kBatch * NT * 4 * ru;
+        x += kBatch * x_step;
         m += kBatch * tok_p;
       }
 #pragma unroll 1
       for (; p < n; ++p) {
-        Weights w;
         const bool here = static_cast<int64_t>(lo + p) * kPiece + 32 * t < a.k;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w.code[h] = make_uint4(0, 0, 0, 0);
-          w.scale[h] = 0;
+          w[0].code[h] = make_uint4(0, 0, 0, 0);
+          w[0].scale[h] = 0;
           if (here) {
-            w.code[h] = load_stream(code[h]);
-            w.scale[h] = load_two(scale[h]);
+            w[0].code[h] = load_stream(code[h]);
+            w[0].scale[h] = load_two(scale[h]);
           }
           code[h] += kPiece / 2;
           scale[h] += kPiece / 16;
         }
-        add_piece(w, x, m);
-        x += NT * 4 * ru;
+        add_piece(w[0], x, m);
+        x += x_step;
         m += tok_p;
       }
 #pragma unroll
@@ -402,19 +419,24 @@ cudaError_t launch(const MatvecArgs& a, cudaStream_t stream) {
 // How the rows and k are split: modelled cycles of an SM whose CTAs are resident at
 // once.  The longer of its pieces (`cycles` each with every warp busy) and of one
 // warp's batches (`wait` each), the rounds in which the tokens are laid out, and
-// what a cluster costs.  Measured (the chosen one first; row warps, splits, CTAs an
-// SM): one token x 12288 x 6144 14.3 us with 2, 1, 3, then 15.3 (1, 1, 3), 17.2 (2, 2,
-// 3), 17.4 (4, 1, 3), 18.4 (1, 1, 2); 16 tokens x 8192 x 8192 20.6 with 8, 2, 1, then
-// 21.9 (16, 2, 1), 29.5 (1, 1, 1), 32.4 (16, 4, 1).
+// what a cluster costs.  Clusters do not find a place on every SM (a group of SMs
+// that share one has 18 to 20): a grid for all 152 ran in two rounds, so one SM in
+// 19 is left out.  Measured, the chosen one first (row warps, splits, CTAs an SM): one
+// token x 12288 x 6144 14.5 us with 2, 1, 3, then 15.8 (4, 2, 3), 16.6 (1, 1, 3); 32 x
+// 6144 x 12288 29.7 with 16, 4, 1, then 33.8 (8, 2, 1), 42 (8, 1, 1); 8 x 8192 x 8192
+// 18.6 with 8, 4, 3, then 20.2 (2, 2, 2), 21.9 (1, 1, 3).
 bool plan(MatvecArgs* a, int nt, int tok_p) {
+  const int per_piece = a->x_codes ? raw_piece_bytes(tok_p) : piece_bytes(nt, tok_p);
+  const int pad = a->x_codes ? tok_p * kRawPad : 0;
   const int cycles = nt == 1 ? 64 : nt == 2 ? 100 : 170;
   const int wait = nt == 1 ? 4000 : nt == 2 ? 5500 : 4500;
   const int warps = 1 << warp_bits(nt);
-  const int64_t sms = device_sm_count();
+  const int64_t all_sms = device_sm_count();
   const int pieces = (a->k + kPiece - 1) / kPiece;
   const int64_t others = static_cast<int64_t>(a->groups) * ((a->tokens + 8 * nt - 1) / (8 * nt));
   int64_t best = -1;
-  for (int s = 1; s <= kMaxSplits && s <= pieces; s *= 2)
+  for (int s = 1; s <= kMaxSplits && s <= pieces; s *= 2) {
+    const int64_t sms = s == 1 ? all_sms : all_sms * 18 / 19;
     for (int res = resident(nt); res >= 1; --res) {
       int64_t blocks = sms * res / (s * others);
       if (blocks < 1) blocks = 1;
@@ -423,13 +445,15 @@ bool plan(MatvecArgs* a, int nt, int tok_p) {
       if (rows > kMaxRows) rows = kMaxRows;
       const int tiles = static_cast<int>((rows + 15) / 16);
       const int slice = (pieces + s - 1) / s;
-      const int stage = slice < stage_tasks(nt) / tok_p ? slice : stage_tasks(nt) / tok_p;
+      int most = a->x_codes ? (kSmemBytes / res - 2048 - pad) * 3 / 4 / per_piece : stage_tasks(nt) / tok_p;
+      if (most < 1) continue;
+      const int stage = slice < most ? slice : most;
       const int64_t rounds = ((a->n + rows - 1) / rows * s * others + sms * res - 1) / (sms * res);
       const int stages = (slice + stage - 1) / stage;
-      const int lays = (stage * tok_p + warps * 16 - 1) / (warps * 16) * stages;
-      for (int bits = 0; bits <= warp_bits(nt); ++bits) {
+      const int lays = a->x_codes ? stages : (stage * tok_p + warps * 16 - 1) / (warps * 16) * stages;
+      for (int bits = warp_bits(nt); bits >= 0; --bits) {
         const int wr = 1 << bits, wk = warps / wr;
-        const int64_t smem = static_cast<int64_t>(stage) * piece_bytes(nt, tok_p) + sum_bytes(tok_p, wk, rows);
+        const int64_t smem = static_cast<int64_t>(stage) * per_piece + pad + sum_bytes(tok_p, wk, rows);
         if (smem > kSmemBytes / res - (res > 1 ? 1024 : 0)) continue;
         const int share = (stage + wk - 1) / wk;
         const int64_t batches = static_cast<int64_t>(stages) * ((tiles + wr - 1) / wr) *
@@ -448,6 +472,7 @@ bool plan(MatvecArgs* a, int nt, int tok_p) {
         }
       }
     }
+  }
   return best >= 0;
 }
 
