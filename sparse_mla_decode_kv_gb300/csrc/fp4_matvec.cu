@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
     stage_tokens(st);
     __syncthreads();
     const int n = share_n(st), lo = stage_lo(st) + share_lo(st);
-    // whole pieces, in batches; the rest one by one
+    // batches of whole pieces, then what is left
     const int whole = max(0, min(n, a.k / kPiece - lo)) / kBatch * kBatch;
 #pragma unroll 1
     for (int tile = 0; tile < (n > 0 ? n_tiles : 0); ++tile) {
@@ -328,22 +328,30 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
         m += kBatch * tok_p;
       }
 #pragma unroll 1
-      for (; p < n; ++p) {
-        const bool here = static_cast<int64_t>(lo + p) * kPiece + 32 * t < a.k;
+      for (; p < n; p += kBatch) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const bool here = p + i < n && static_cast<int64_t>(lo + p + i) * kPiece + 32 * t < a.k;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            w[i].code[h] = make_uint4(0, 0, 0, 0);
+            w[i].scale[h] = 0;
+            if (here) {
+              w[i].code[h] = load_stream(code[h] + i * (kPiece / 2));
+              w[i].scale[h] = load_two(scale[h] + i * (kPiece / 16));
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i == 0 || p + i < n) add_piece(w[i], x + i * x_step, m + i * tok_p);  // uniform over the warp
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w[0].code[h] = make_uint4(0, 0, 0, 0);
-          w[0].scale[h] = 0;
-          if (here) {
-            w[0].code[h] = load_stream(code[h]);
-            w[0].scale[h] = load_two(scale[h]);
-          }
-          code[h] += kPiece / 2;
-          scale[h] += kPiece / 16;
+          code[h] += kBatch * (kPiece / 2);
+          scale[h] += kBatch * (kPiece / 16);
         }
-        add_piece(w[0], x, m);
-        x += x_step;
-        m += tok_p;
+        x += kBatch * x_step;
+        m += kBatch * tok_p;
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -457,7 +465,7 @@ bool plan(MatvecArgs* a, int nt, int tok_p) {
         if (smem > kSmemBytes / res - (res > 1 ? 1024 : 0)) continue;
         const int share = (stage + wk - 1) / wk;
         const int64_t batches = static_cast<int64_t>(stages) * ((tiles + wr - 1) / wr) *
-                                (share / batch(nt) + (share % batch(nt) + 1) / 2);
+                                ((share + batch(nt) - 1) / batch(nt));
         const int64_t work = static_cast<int64_t>(res) * tiles * slice * cycles;
         const int64_t cost =
             rounds * ((work > batches * wait ? work : batches * wait) + lays * 4000 + (s > 1 ? 3500 + 500 * s : 0));
