@@ -17,11 +17,11 @@
 // operand of its product.  A CTA an SM takes units until none is left: the grid
 // has one CTA a unit, and a running one cancels the next that has not started and
 // takes its place, so the next unit's copies and first products overlap the end of
-// this one's.  Warp 0 issues the products, warp 1 the copies, warp 2 looks through
-// the values that some row must not see, warp 3 finds the units, and two groups of
-// four warps have a tile's softmax, a thread a row: maximum and sum stay in
-// registers.  Products of one issuing thread complete in order, so a full S says
-// that the product before it, which read P and V, is done too.  Slices' partial
+// this one's.  A warp for each tile issues its products, one finds the units and
+// copies, one looks through the values that some row must not see, and two groups
+// of four warps have a tile's softmax, a thread a row: maximum and sum stay in
+// registers.  A tile's products have one issuing thread and complete in order, so a
+// full S says that the product before it, which read P and V, is done too.  Slices' partial
 // outputs are joined by their LSEs in a second kernel.
 //
 // Values that a row must not see.  A weight of 0 does not keep an infinity or
@@ -45,7 +45,9 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 128;    // rows of a tile, and keys of one
-constexpr int kMmaWarp = 0, kCopyWarp = 1, kUnitWarp = 3, kFirstSoftmax = 4;  // warp 2: the values
+// Warps 0 and 3 issue the products of tile 0 and 1, warp 1 finds the units and copies,
+// warp 2 searches the values.
+constexpr int kMmaWarp = 0, kCopyWarp = 1, kCleanWarp = 2, kFirstSoftmax = 4;
 constexpr int kThreads = 12 * 32;
 constexpr int kChunkBytes = kTile * 128;  // 128 rows of 64 values
 constexpr int kItems = 16;                // barriers of copied tiles (keys and values in turn)
@@ -81,7 +83,7 @@ struct Ctl {
   uint64_t q_full[2], q_free[2];
   uint64_t full[kItems], free_[kItems];  // copied tiles
   uint64_t ready[kItems / 2];            // values that have been searched
-  uint64_t s_full[2], p_full[2][2], o_full[2], done, canceled, wanted;
+  uint64_t s_full[2], p_full[2][2], o_full[2], done[2], canceled;
   uint4 answer;  // to the request for another unit
   Unit unit[kUnits];
   uint32_t tmem_base;
@@ -96,12 +98,14 @@ __host__ __device__ constexpr int ring_chunks() {
   return (kSmemBytes - kCtlBytes - 1024 - 2 * KC * kChunkBytes) / kChunkBytes;
 }
 
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+// 64 columns of this warp's 32 lanes and their largest value (NaN left out); complete
+// behind tmem_wait.
+__device__ __forceinline__ void tmem_ld64_max(uint32_t taddr, uint32_t (&r)[64], float& top) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
       "%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -109,7 +113,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
         "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
         "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
         "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=f"(top)
       : "r"(taddr)
       : "memory");
 }
@@ -122,7 +126,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 // All loads of this thread have come; r's first use stays behind it.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[64]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[64], float& top) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
       : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
         "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
@@ -131,7 +135,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[64]) {
         "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
         "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
         "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
-        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63]), "+f"(top)
       :
       : "memory");
 }
@@ -180,11 +184,6 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
   return e != 0;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 // Two floats at a time (the packed forms issue once for both).
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -319,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&sm.unit_full[i], 1);
-      mbar_init(&sm.unit_free[i], 3 + 8);
+      mbar_init(&sm.unit_free[i], 3 + 8);  // both products' warps, the searching one, the softmax's
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
@@ -328,15 +327,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.p_full[i][0], 4);
       mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.done[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.free_[i], 1);
+      mbar_init(&sm.free_[i], 2);
     }
     for (int i = 0; i < kItems / 2; ++i) mbar_init(&sm.ready[i], 1);
-    mbar_init(&sm.done, 1);
     mbar_init(&sm.canceled, 1);
-    mbar_init(&sm.wanted, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -359,29 +357,68 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kFirstSoftmax) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-    if (warp == kUnitWarp) {
-      // ---------------------------------------------------------- units
+    if (warp == kCopyWarp) {
+      // ---------------------------------------------------------- units and copies
+      const bool leader = elect_one();
+      int issued = 0, freed = 0;  // items (the leader's)
+      int at = 0, at_freed = 0;   // first chunk of the next item, and of the next that will be free
+      uint32_t q_uses[2] = {0, 0};
       int id = blockIdx.x, n = 0;
       bool ok = true;
-      for (uint32_t asked = 0, found = 0; ok && id >= 0; ++asked) {
+      for (uint32_t asked = 0; ok && id >= 0; ++asked) {
         Unit u;
         if (find_unit(args, id, lane, u)) {
           if (n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
-          if (ok && lane == 0) {
+          if (ok && leader) {
             sm.unit[n % kUnits] = u;
             sm.any_bad[n % kUnits] = 0;
             for (int i = 0; i < kMaskedTiles * (kTile / 32); ++i) sm.bad[n % kUnits][0][i] = 0;
             mbar_arrive(&sm.unit_full[n % kUnits]);
+            const int items = 2 * max(u.count[0], u.count[1]);
+            auto copy_q = [&](int s) {
+              if (q_uses[s] > 0) ok = wait_bar(sm, &sm.q_free[s], (q_uses[s] - 1) & 1u, fw);
+              if (!ok) return;
+              mbar_expect_tx(&sm.q_full[s], static_cast<uint32_t>(KC * rows * 128));
+              ++q_uses[s];
+              for (int c = 0; c < KC; ++c)
+                tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, u.head * args.group, u.q0 + u.tok + s * per,
+                            &sm.q_full[s]);
+            };
+            for (int i = 0; i < items && ok; ++i) {
+              const int chunks = (i & 1) ? VC : KC;
+              // the items before this one whose places it takes
+              while (ok && at_freed < at + chunks - kRing) {
+                ok = wait_bar(sm, &sm.free_[freed % kItems], parity(freed), fw);
+                at_freed += (freed & 1) ? VC : KC;
+                ++freed;
+              }
+              if (!ok) break;
+              uint64_t* const bar = &sm.full[issued % kItems];
+              mbar_expect_tx(bar, static_cast<uint32_t>(chunks * kChunkBytes));
+              for (int c = 0; c < chunks; ++c)
+                tma_load_3d(s_ring + (at + c) % kRing * kChunkBytes, (i & 1) ? &v_map : &k_map, 64 * c, u.head,
+                            u.k0 + (u.begin + (i >> 1)) * kTile, bar);
+              ++issued;
+              at += chunks;
+              if (at >= 2 * kRing && at_freed >= kRing) {  // both count from the same round of the ring
+                at -= kRing;
+                at_freed -= kRing;
+              }
+              if (i == 0) {
+                if (u.count[0] > 0) copy_q(0);
+                if (ok && u.count[1] > 0) copy_q(1);
+              }
+            }
           }
+          __syncwarp();
+          ok = __all_sync(0xFFFFFFFFu, ok);
           ++n;
-          // The next one is asked for when this one's last copies have been started, two
-          // or three tiles before its end: a long unit's successor is for whoever is free
-          // first (asked for at once, 6000 tokens x 16 heads took 172 us).
-          if (ok) ok = wait_bar_warp(sm, &sm.wanted, found & 1u, fw);
-          ++found;
         }
         if (!ok) break;
-        if (lane == 0) {
+        // The next unit is asked for when this one's last copies have been started, two
+        // or three tiles before its end: a long unit's successor is for whoever is free
+        // first (asked for at once, 6000 tokens x 16 heads took 172 us for 156).
+        if (leader) {
           mbar_expect_tx(&sm.canceled, 16);
           request_unit(&sm.answer, &sm.canceled);
         }
@@ -392,61 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (ok && n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
-      if (ok && lane == 0) {
-        sm.unit[n % kUnits].last = 1;
-        mbar_arrive(&sm.unit_full[n % kUnits]);
-      }
-      __syncwarp();
-    } else if (warp == kCopyWarp) {
-      // ---------------------------------------------------------- copies
-      if (elect_one()) {
-        int issued = 0, freed = 0;                  // items
-        int at = 0, at_freed = 0;                   // first chunk of the next item, and of the next that will be free
-        uint32_t q_uses[2] = {0, 0};
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-          ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
-          if (!ok) break;
-          const Unit& u = sm.unit[n % kUnits];
-          if (u.last) break;
-          const int q_row = u.q0 + u.tok, k_row = u.k0 + u.begin * kTile, head = u.head;
-          const int counts[2] = {u.count[0], u.count[1]};
-          mbar_arrive(&sm.unit_free[n % kUnits]);
-          const int items = 2 * max(counts[0], counts[1]);
-          auto copy_q = [&](int s) {
-            if (q_uses[s] > 0) ok = wait_bar(sm, &sm.q_free[s], (q_uses[s] - 1) & 1u, fw);
-            if (!ok) return;
-            mbar_expect_tx(&sm.q_full[s], static_cast<uint32_t>(KC * rows * 128));
-            ++q_uses[s];
-            for (int c = 0; c < KC; ++c)
-              tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, head * args.group, q_row + s * per, &sm.q_full[s]);
-          };
-          for (int i = 0; i < items && ok; ++i) {
-            const int chunks = (i & 1) ? VC : KC;
-            // the items before this one whose places it takes
-            while (ok && at_freed < at + chunks - kRing) {
-              ok = wait_bar(sm, &sm.free_[freed % kItems], parity(freed), fw);
-              at_freed += (freed & 1) ? VC : KC;
-              ++freed;
-            }
-            if (!ok) break;
-            uint64_t* const bar = &sm.full[issued % kItems];
-            mbar_expect_tx(bar, static_cast<uint32_t>(chunks * kChunkBytes));
-            for (int c = 0; c < chunks; ++c)
-              tma_load_3d(s_ring + (at + c) % kRing * kChunkBytes, (i & 1) ? &v_map : &k_map, 64 * c, head,
-                          k_row + (i >> 1) * kTile, bar);
-            ++issued;
-            at += chunks;
-            if (at >= 2 * kRing && at_freed >= kRing) {  // both count from the same round of the ring
-              at -= kRing;
-              at_freed -= kRing;
-            }
-            if (i == 0) {
-              if (counts[0] > 0) copy_q(0);
-              if (ok && counts[1] > 0) copy_q(1);
-            }
-          }
-          if (ok) mbar_arrive(&sm.wanted);
+      if (leader) {
+        if (ok) {
+          sm.unit[n % kUnits].last = 1;
+          mbar_arrive(&sm.unit_full[n % kUnits]);
         }
         // no copy may be in flight when the CTA leaves
         for (int s = 0; s < 2; ++s)
@@ -455,46 +441,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_bounded(&sm.full[i % kItems], parity(i), fw, kFaultPromptWait);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------- products
+    } else if (warp != kCleanWarp) {
+      // ---------------------------------------------------------- products of tile s
+      const int s = warp == kMmaWarp ? 0 : 1;
       const uint32_t idesc_s = bf16_idesc(kTile, args.negate, false);
       constexpr uint32_t idesc_o = bf16_idesc(64 * VC, false, true);
       if (elect_one()) {
-        const uint64_t q_desc = umma_desc_sw128(smem_u32(s_q));
+        const uint64_t q_desc = umma_desc_sw128(smem_u32(s_q) + s * KC * kChunkBytes);
         const uint32_t ring = smem_u32(s_ring);
+        const uint32_t d_s = kSCol + kTile * s, d_o = kOCol + kTile * s;
         int item = 0, at = 0;  // the unit's first item and its first chunk's place in the ring
-        uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+        uint32_t q_uses = 0, p_uses = 0;
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
           ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
           if (!ok || sm.unit[n % kUnits].last) break;
-          const int count[2] = {sm.unit[n % kUnits].count[0], sm.unit[n % kUnits].count[1]};
+          const int count = s == 0 ? sm.unit[n % kUnits].count[0] : sm.unit[n % kUnits].count[1];
+          const int n_tiles = max(count, s == 0 ? sm.unit[n % kUnits].count[1] : sm.unit[n % kUnits].count[0]);
           mbar_arrive(&sm.unit_free[n % kUnits]);
-          const int n_tiles = max(count[0], count[1]);
           if (n_tiles == 0) continue;
-          auto scores = [&](int s, int j, int k_at) {  // S of tile s and keys j, which begin at chunk k_at
+          auto scores = [&](int j, int k_at) {  // S of keys j, which begin at chunk k_at
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
               const int chunk = k_at + c >= kRing ? k_at + c - kRing : k_at + c;
               const uint64_t k_desc = umma_desc_sw128(ring + chunk * kChunkBytes);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                umma_ss(kSCol + kTile * s, q_desc + (((s * KC + c) * kChunkBytes + 32 * i) >> 4), k_desc + (32 * i >> 4),
-                        idesc_s, c > 0 || i > 0);
+                umma_ss(d_s, q_desc + ((c * kChunkBytes + 32 * i) >> 4), k_desc + (32 * i >> 4), idesc_s, c > 0 || i > 0);
             }
             umma_commit(&sm.s_full[s]);
-            if (j + 1 == count[s]) umma_commit(&sm.q_free[s]);
+            if (j + 1 == count) umma_commit(&sm.q_free[s]);
           };
           ok = wait_bar(sm, &sm.full[item % kItems], parity(item), fw);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (!ok || count[s] == 0) continue;
-            ok = wait_bar(sm, &sm.q_full[s], q_uses[s] & 1u, fw);
-            ++q_uses[s];
-            if (!ok) continue;
-            tcgen05_fence_after();
-            scores(s, 0, at);
+          if (ok && count > 0) {
+            ok = wait_bar(sm, &sm.q_full[s], q_uses & 1u, fw);
+            ++q_uses;
+            if (ok) {
+              tcgen05_fence_after();
+              scores(0, at);
+            }
           }
           umma_commit(&sm.free_[item % kItems]);
 #pragma unroll 1
@@ -504,50 +490,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             v_at = v_at >= kRing ? v_at - kRing : v_at;
             k_at = k_at >= kRing ? k_at - kRing : k_at;
             ok = wait_bar(sm, &sm.ready[v_item / 2 % (kItems / 2)], parity(v_item), fw);
-            if (ok && j + 1 < n_tiles) ok = wait_bar(sm, &sm.full[k_item % kItems], parity(k_item), fw);
+            if (ok && j < count) {
+              // the product of the first half of the keys runs while the other's weights
+              // are computed
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (ok && j < count[s]) {
-                // the product of the first half of the keys runs while the other's weights
-                // are computed
+              for (int half = 0; half < 2; ++half) {
+                if (ok) ok = wait_bar(sm, &sm.p_full[s][half], p_uses & 1u, fw);
+                if (!ok) continue;
+                tcgen05_fence_after();
+                // the two chunks of a value tile may lie at the ring's two ends
+                const uint32_t v0 = ring + v_at * kChunkBytes;
+                if (VC == 1 || v_at + 1 < kRing) {
+                  const uint64_t v_desc = desc_values(v0);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  if (ok) ok = wait_bar(sm, &sm.p_full[s][half], p_uses[s] & 1u, fw);
-                  if (!ok) continue;
-                  tcgen05_fence_after();
-                  // the two chunks of a value tile may lie at the ring's two ends
-                  const uint32_t v0 = ring + v_at * kChunkBytes;
-                  if (VC == 1 || v_at + 1 < kRing) {
-                    const uint64_t v_desc = desc_values(v0);
+                  for (int i = 4 * half; i < 4 * half + 4; ++i)
+                    umma_ts(d_o, d_s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, j > 0 || i > 0);
+                } else {
+#pragma unroll
+                  for (int c = 0; c < VC; ++c) {
+                    const uint64_t v_desc = desc_values(c == 0 ? v0 : ring);
 #pragma unroll
                     for (int i = 4 * half; i < 4 * half + 4; ++i)
-                      umma_ts(kOCol + kTile * s, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, j > 0 || i > 0);
-                  } else {
-#pragma unroll
-                    for (int c = 0; c < VC; ++c) {
-                      const uint64_t v_desc = desc_values(c == 0 ? v0 : ring);
-#pragma unroll
-                      for (int i = 4 * half; i < 4 * half + 4; ++i)
-                        umma_ts(kOCol + kTile * s + 64 * c, kSCol + kTile * s + 8 * i, v_desc + (2048 * i >> 4),
-                                bf16_idesc(64, false, true), j > 0 || i > 0);
-                    }
+                      umma_ts(d_o + 64 * c, d_s + 8 * i, v_desc + (2048 * i >> 4), bf16_idesc(64, false, true),
+                              j > 0 || i > 0);
                   }
                 }
-                ++p_uses[s];
-                if (ok) {
-                  if (j + 1 == count[s]) umma_commit(&sm.o_full[s]);
-                }
               }
-              if (s == 1) umma_commit(&sm.free_[v_item % kItems]);
-              if (ok && j + 1 < count[s]) scores(s, j + 1, k_at);
+              ++p_uses;
+              if (ok && j + 1 == count) umma_commit(&sm.o_full[s]);
             }
-            if (j + 1 < n_tiles) umma_commit(&sm.free_[k_item % kItems]);
+            umma_commit(&sm.free_[v_item % kItems]);
+            if (ok && j + 1 < n_tiles) {
+              ok = wait_bar(sm, &sm.full[k_item % kItems], parity(k_item), fw);
+              if (ok && j + 1 < count) scores(j + 1, k_at);
+              umma_commit(&sm.free_[k_item % kItems]);
+            }
             item += 2;
             at = k_at;
           }
         }
-        umma_commit(&sm.done);
-        mbar_wait_bounded(&sm.done, 0u, fw, kFaultPromptWait);
+        umma_commit(&sm.done[s]);
+        mbar_wait_bounded(&sm.done[s], 0u, fw, kFaultPromptWait);
       }
       __syncwarp();
     } else {
@@ -643,26 +626,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tcgen05_fence_after();
         uint32_t z[2][64];
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld64(s_addr, z[0]);
-        tmem_wait(z[0]);
-        tmem_ld64(s_addr + 64, z[1]);  // on its way while the first half's maximum is taken
+        float most[2];
+        tmem_ld64_max(s_addr, z[0], most[0]);
+        tmem_ld64_max(s_addr + 64, z[1], most[1]);
+        tmem_wait(z[0], most[0]);
+        tmem_wait(z[1], most[1]);
+        if (begin + j >= tile_full) {
+          const int rel = lim - (begin + j) * kTile;
+          most[0] = most[1] = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) tmem_wait(z[1]);
-          if (begin + j >= tile_full) {
-            const int rel = lim - (begin + j) * kTile - 64 * half;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= rel) z[half][i] = 0xFF800000u;
+          for (int i = 0; i < kTile; ++i) {
+            if (i >= rel) z[i >> 6][i & 63] = 0xFF800000u;
+            most[i & 1] = fmaxf(most[i & 1], __uint_as_float(z[i >> 6][i & 63]));
           }
-#pragma unroll
-          for (int i = 0; i < 64; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              m[k] = max3(m[k], __uint_as_float(z[half][i + k]), __uint_as_float(z[half][i + 4 + k]));
         }
-        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * sl;
+        const float top = fmaxf(most[0], most[1]) * sl;
         const bool raise = top - ref > kLag;
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float alpha = 1.f;
