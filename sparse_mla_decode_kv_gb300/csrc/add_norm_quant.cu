@@ -45,6 +45,9 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) add_norm_quant_kernel(co
   constexpr int kRes = R == kFloat ? 2 : R == kBf16 ? 1 : 0;  // 16-byte loads of the residual a chunk
   __shared__ float s_sum[2][kWarps];
   __shared__ uint32_t s_max[2][kWarps];
+  // Plain loads from here on: the grid may be resident before its inputs are written.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int team = threadIdx.x / kLanes, tl = threadIdx.x % kLanes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = a.dim / 8;
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) add_norm_quant_kernel(co
     for (int c = 0; c < C; ++c) {
       const int i = tl + c * kLanes;
       float w[8];
-      unpack8(i < chunks ? __ldg(reinterpret_cast<const uint4*>(a.weight) + i) : make_uint4(0, 0, 0, 0), w);
+      unpack8(i < chunks ? reinterpret_cast<const uint4*>(a.weight)[i] : make_uint4(0, 0, 0, 0), w);
       mx[c] = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -212,12 +215,22 @@ cudaError_t launch(const AddNormArgs& a, cudaStream_t stream) {
   const int64_t need = (a.tokens + kTeams - 1) / kTeams;
   const int64_t room = static_cast<int64_t>(device_sm_count()) * (W > 8 ? 2 : 4);
   const unsigned grid = static_cast<unsigned>(need < room ? need : room);
-  switch (a.residual_type) {
-    case kNone: add_norm_quant_kernel<W, C, kNone><<<grid, 32 * kWarps, 0, stream>>>(a); break;
-    case kBf16: add_norm_quant_kernel<W, C, kBf16><<<grid, 32 * kWarps, 0, stream>>>(a); break;
-    default: add_norm_quant_kernel<W, C, kFloat><<<grid, 32 * kWarps, 0, stream>>>(a); break;
-  }
-  return cudaGetLastError();
+  const void* kernel = a.residual_type == kNone   ? reinterpret_cast<const void*>(add_norm_quant_kernel<W, C, kNone>)
+                       : a.residual_type == kBf16 ? reinterpret_cast<const void*>(add_norm_quant_kernel<W, C, kBf16>)
+                                                  : reinterpret_cast<const void*>(add_norm_quant_kernel<W, C, kFloat>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  AddNormArgs args = a;
+  void* params[] = {&args};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, params);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
