@@ -9,6 +9,7 @@ not built, loading fails with an explicit error.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Optional
 
@@ -87,8 +88,8 @@ SIGNATURES = {
     "mla_prefix_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F32,
                                  _I32, _P, _P, _P, _SZ, _P]),
     "mla_prompt_attention_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I32]),
-    "mla_prompt_attention": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32, _I32,
-                                    _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "mla_prompt_attention": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32,
+                                    _I32, _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "mla_add_norm_quant": (_I32, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _F32, _P, _P, _P]),
     "mla_fp4_matvec": (_I32, [_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I32, _I64, _I64,
                               _P]),
@@ -470,6 +471,11 @@ def _c_int(v, name) -> None:
         raise ValueError(f"{name} {v} does not fit 32 bits")
 
 
+def _c_ints(**values) -> None:
+    for name, v in values.items():
+        _c_int(v, name)
+
+
 def _length(v, name) -> int:
     """A length cut to the longest that a context can have."""
     if v < 0:
@@ -702,6 +708,12 @@ def mla_prompt_attention_workspace_size(q_tokens: int, kv_tokens: int, batch: in
     return int(load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim))
 
 
+@functools.lru_cache(maxsize=1024)
+def _prompt_workspace(device, *sizes) -> int:
+    """The size for the current device (its number is part of the key), without a call into the library."""
+    return int(load().mla_prompt_attention_workspace_size(*sizes))
+
+
 def mla_prompt_attention(q, k, v, query_start, kv_start, softmax_scale, causal=True, out=None, lse=None,
                          workspace=None, stream=None):
     """Attention of packed sequences: b's query tokens are query_start[b] ..
@@ -720,17 +732,22 @@ def mla_prompt_attention(q, k, v, query_start, kv_start, softmax_scale, causal=T
     batch = _contig(query_start, torch.int32, "query_start").numel() - 1
     if batch < 0 or _contig(kv_start, torch.int32, "kv_start").numel() != batch + 1:
         raise ValueError("query_start and kv_start must have one entry for each sequence and one more")
+    if max(batch, heads, kv_heads, dk, dv) > _INT_MAX:
+        _c_ints(batch=batch, heads=heads, kv_heads=kv_heads, dk=dk, dv=dv)
     if out is None:
         out = _new(q, (q_tokens, heads, dv), torch.bfloat16, stream)
-    elif out.shape != (q_tokens, heads, dv):
-        raise ValueError(f"out: expected shape {(q_tokens, heads, dv)}, got {tuple(out.shape)}")
-    out_token, out_head, _ = _head_strides(out, "out")
+        out_token, out_head = heads * dv, dv
+    else:
+        if out.shape != (q_tokens, heads, dv):
+            raise ValueError(f"out: expected shape {(q_tokens, heads, dv)}, got {tuple(out.shape)}")
+        out_token, out_head, _ = _head_strides(out, "out")
     if lse is not None:
         _take(lse, (q_tokens, heads), torch.float32, "lse", q, stream)
     if workspace is None:
-        need = load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, heads, kv_heads, dv)
-        workspace = _new(q, (need,), torch.uint8, stream) if need > 0 else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = _prompt_workspace(device, q_tokens, kv_tokens, batch, heads, kv_heads, dv)
+        workspace = _new(q, (ws_bytes,), torch.uint8, stream) if ws_bytes > 0 else None
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     _check("mla_prompt_attention",
            load().mla_prompt_attention(q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head, v.data_ptr(),
                                        v_token, v_head, query_start.data_ptr(), kv_start.data_ptr(), batch, q_tokens,
@@ -741,12 +758,13 @@ def mla_prompt_attention(q, k, v, query_start, kv_start, softmax_scale, causal=T
 
 
 def _rows(t, dtype, name):
-    """Row stride of a [n, dim] tensor whose last axis is contiguous."""
+    """(shape, row stride) of a [n, dim] tensor whose last axis is contiguous."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel() > 0):
+    shape, strides = t.shape, t.stride()
+    if len(strides) != 2 or (strides[1] != 1 and shape[1] > 1 and t.numel() > 0):
         raise ValueError(f"{name} must be [n, dim] with a contiguous last axis")
-    return t.stride(0)
+    return shape, strides[0]
 
 
 def _bytes(t, name):
@@ -764,25 +782,30 @@ def mla_add_norm_quant(x, weight, residual=None, eps=1e-6, group=128, codes=None
     (codes float8_e4m3fn [n, D], scales [n, ceil(D / 128) or 1], h in the
     residual's type or None); residual_out may be residual."""
     device = _here(x, weight, residual, codes, scales, None if residual is None else residual_out)
-    x_stride = _rows(x, torch.bfloat16, "x")
-    n, dim = x.shape
+    shape, x_stride = _rows(x, torch.bfloat16, "x")
+    n, dim = shape
     if _contig(weight, torch.bfloat16, "weight").numel() != dim:
         raise ValueError(f"weight must have one value for each of {dim} dims")
     _c_int(group, "group")
+    _c_int(dim, "dim")
     res_type = res_stride = out_stride = 0
     if residual is not None:
-        if residual.dtype is not torch.bfloat16 and residual.dtype is not torch.float32:
-            raise TypeError(f"residual: expected torch.bfloat16 or torch.float32, got {residual.dtype}")
-        res_type = 1 if residual.dtype is torch.bfloat16 else 2
-        res_stride = _rows(residual, residual.dtype, "residual")
+        kind = residual.dtype
+        if kind is not torch.bfloat16 and kind is not torch.float32:
+            raise TypeError(f"residual: expected torch.bfloat16 or torch.float32, got {kind}")
+        res_type = 1 if kind is torch.bfloat16 else 2
+        res_shape, res_stride = _rows(residual, kind, "residual")
         if residual_out is None:
-            residual_out = _new(residual, (n, dim), residual.dtype, stream)
-        out_stride = _rows(residual_out, residual.dtype, "residual_out")
-        if residual.shape != x.shape or residual_out.shape != x.shape:
-            raise ValueError("residual and residual_out must be shaped like x")
+            residual_out, out_stride = _new(residual, shape, kind, stream), dim
+        else:
+            out_shape, out_stride = _rows(residual_out, kind, "residual_out")
+            if out_shape != shape:
+                raise ValueError("residual_out must be shaped like x")
+        if res_shape != shape:
+            raise ValueError("residual must be shaped like x")
     if codes is None:
-        codes = _new(x, (n, dim), torch.float8_e4m3fn, stream)
-    elif _bytes(codes, "codes").shape != x.shape:
+        codes = _new(x, shape, torch.float8_e4m3fn, stream)
+    elif _bytes(codes, "codes").shape != shape:
         raise ValueError("codes must be shaped like x")
     scales = _take(scales, (n, -(-dim // group) if group > 0 else 1), torch.float32, "scales", x, stream)
     _check("mla_add_norm_quant",
@@ -809,43 +832,46 @@ def mla_fp4_matvec(x, codes, scales, weight_scale=None, x_scales=None, out=None,
     for each matrix, or None.  Returns out [T, N] or [T, G, N], bf16 or float32."""
     device = _here(x, codes, scales, weight_scale, x_scales, out)
     x_token, x_group = _token_groups(x, "x")
-    shape = x.shape
+    shape, c_shape, kind = x.shape, _contig(codes, torch.uint8, "codes").shape, x.dtype
     tokens, k = shape[0], shape[-1]
     groups = shape[1] if len(shape) == 3 else 1
-    _contig(codes, torch.uint8, "codes")
-    _bytes(scales, "scales")
-    if codes.dim() != len(shape) or codes.shape[-1] * 2 != k or k % 16 != 0 or \
-            (len(shape) == 3 and codes.shape[0] != groups):
-        raise ValueError(f"codes {tuple(codes.shape)} do not fit x {tuple(shape)}: [N, K / 2] or [G, N, K / 2]")
-    n = codes.shape[-2]
-    if scales.shape != (*codes.shape[:-1], k // 16):
+    if len(c_shape) != len(shape) or c_shape[-1] * 2 != k or k % 16 != 0 or (len(shape) == 3 and c_shape[0] != groups):
+        raise ValueError(f"codes {tuple(c_shape)} do not fit x {tuple(shape)}: [N, K / 2] or [G, N, K / 2]")
+    n = c_shape[-2]
+    if max(n, k, groups) > _INT_MAX:
+        _c_ints(n=n, k=k, groups=groups)
+    if _bytes(scales, "scales").shape != (*c_shape[:-1], k // 16):
         raise ValueError("scales must have one value for 16 codes")
     if weight_scale is not None and _contig(weight_scale, torch.float32, "weight_scale").numel() != groups:
         raise ValueError(f"weight_scale must have one value for each of {groups} matrices")
     scale_groups = 0
-    if x.dtype is torch.float8_e4m3fn:
+    if kind is torch.float8_e4m3fn:
         if x_scales is None:
             raise ValueError("x in 8 bits needs x_scales")
-        _contig(x_scales, torch.float32, "x_scales")
-        scale_groups = x_scales.shape[-1] if x_scales.dim() > 0 else 0
-        if x_scales.shape[:-1] != shape[:-1] or scale_groups not in (1, -(-k // 128)):
+        s_shape = _contig(x_scales, torch.float32, "x_scales").shape
+        scale_groups = s_shape[-1] if len(s_shape) > 0 else 0
+        if s_shape[:-1] != shape[:-1] or scale_groups not in (1, -(-k // 128)):
             raise ValueError("x_scales must have one value for 128 of x's, or one for each of its rows")
-    elif x.dtype is not torch.bfloat16:
-        raise TypeError(f"x: expected torch.bfloat16 or torch.float8_e4m3fn, got {x.dtype}")
+    elif kind is not torch.bfloat16:
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
     elif x_scales is not None:
         raise ValueError("x_scales belong to x in 8 bits")
+    out_shape = (*shape[:-1], n)
     if out is None:
         if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise TypeError(f"out_dtype: expected torch.bfloat16 or torch.float32, got {out_dtype}")
-        out = _new(x, (*shape[:-1], n), out_dtype, stream)
-    elif out.shape != (*shape[:-1], n):
-        raise ValueError(f"out: expected shape {(*shape[:-1], n)}, got {tuple(out.shape)}")
-    elif out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
-        raise TypeError(f"out: expected torch.bfloat16 or torch.float32, got {out.dtype}")
-    out_token, out_group = _token_groups(out, "out")
+        out = _new(x, out_shape, out_dtype, stream)
+        out_token, out_group = groups * n, n
+    else:
+        out_dtype = out.dtype
+        if out.shape != out_shape:
+            raise ValueError(f"out: expected shape {out_shape}, got {tuple(out.shape)}")
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+            raise TypeError(f"out: expected torch.bfloat16 or torch.float32, got {out_dtype}")
+        out_token, out_group = _token_groups(out, "out")
     _check("mla_fp4_matvec",
            load().mla_fp4_matvec(x.data_ptr(), 1 if scale_groups else 0, x_token, x_group, _at(x_scales), scale_groups,
                                  codes.data_ptr(), scales.data_ptr(), _at(weight_scale), tokens, groups, n, k,
-                                 out.data_ptr(), 1 if out.dtype is torch.float32 else 0, out_token, out_group,
+                                 out.data_ptr(), 1 if out_dtype is torch.float32 else 0, out_token, out_group,
                                  _on(stream, device)))
     return out
