@@ -21,8 +21,17 @@
 // copies, one looks through the values that some row must not see, and two groups
 // of four warps have a tile's softmax, a thread a row: maximum and sum stay in
 // registers.  A tile's products have one issuing thread and complete in order, so a
-// full S says that the product before it, which read P and V, is done too.  Slices' partial
-// outputs are joined by their LSEs in a second kernel.
+// full S says that the product before it, which read P and V, is done too.  Slices'
+// partial outputs are joined by their LSEs in a second kernel.
+//
+// What bounds it.  Over many keys power (1,380 of 1,400 W) and the chain score,
+// softmax, product of each tile, which the other tile's hides in part: 16,384 tokens
+// x 16 heads x 192 / 128 causal 805 us, 1,710 TFLOP/s, of 128 / 128 693 us, 1,590;
+// 6,000 x 192 / 128 134 us, 1,370 (the tensor pipe active in 61 % of the cycles).
+// The same with one CTA a unit 163, units taken in turn 156, a product warp a tile
+// and maxima from the loads 144, exponentials in turn 134.  Short prompts (16 packed
+// ones of up to 1,500 tokens, 160 us) pay each unit's last softmax and output, 3 to 4
+// us; single tokens walk memory: one over 100,000 keys x 16 heads 163 us, 6,250 GB/s.
 //
 // Values that a row must not see.  A weight of 0 does not keep an infinity or
 // NaN out of a product.  Where some row's mask cuts a tile of keys, its values are
@@ -56,6 +65,7 @@ constexpr int kSmemBytes = 227 * 1024;
 constexpr int kCtlBytes = 1024;
 constexpr uint32_t kSCol = 0, kOCol = 256, kTmemCols = 512;
 constexpr int kTurnPolls = 40;  // of about 30 cycles
+constexpr int64_t kMaxSlice = 65536;  // tiles of keys
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Tiles of keys that some of a CTA's rows see and others do not: what its up to 256
@@ -314,9 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32 * kCopyWarp)
     for (const CUtensorMap* m : {&q_map, &k_map, &v_map})
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   const int per = kTile / args.group, rows = per * args.group;  // tokens and rows of a tile
   if (threadIdx.x == 0) {
     for (int i = 0; i < kUnits; ++i) {
@@ -353,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tcgen05_fence_after();
   // all 512 tensor-memory columns were allocated: they start at column 0
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // inputs may be written until here
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Copied tiles in turn, over all units: an even item has the keys of a tile, the next
   // one its values.  Their chunks follow one another around the ring.
@@ -668,9 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The two tiles' warps of a scheduler take turns, so that one tile's exponentials run
         // beside the other's products and not beside its exponentials.  A hint: who has
-        // waited long enough goes on.  It pays over many tiles of keys: 16,384 tokens x 16
-        // heads of 192 798 us (870 without), of 128 693 (773), 6,000 of 192 134 (144); 16
-        // sequences of up to 1,500 170 (162), 32 single tokens 132 (125).
+        // waited long enough goes on.  It pays over many tiles of keys (x 16 heads, with
+        // and without): 16,384 tokens of 192 dims 805 and 868 us, of 128 693 and 767, 6,000
+        // of 192 134 and 142; 2 x 4,096 of 128 124 and 118, 2 x 3,000 of 192 91 and 85.
         if (kTurns) {
           for (int i = 0; i < kTurnPolls && *reinterpret_cast<volatile int*>(&sm.busy[s ^ 1][quad]) != 0; ++i) {
           }
@@ -906,6 +915,10 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
     }
     if (units * n > 8 * sms) break;
   }
+  // A tile without rows waits for as long as the other's whole slice: no slice may last as
+  // long as a bounded wait (a tile of keys takes about 2 us, the wait a second at most).
+  const int64_t least = ((kv_tokens + kTile - 1) / kTile + kMaxSlice - 1) / kMaxSlice;
+  if (p.splits < least) p.splits = static_cast<int>(least);
   if (p.splits > 1)
     p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 1) * sizeof(float) + 255) / 256 * 256;
   return p;
@@ -935,9 +948,9 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
                encode_tensor_map_3d(&v, have ? a.v : a.q, a.dv, a.kv_heads, kv_rows, 2 * a.v_head, 2 * a.v_token, 1, kTile);
   if (!*described) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(plan.places * a.kv_heads * a.splits);
-  // both tiles filled, and 16 tiles of keys or more, on average
+  // both tiles filled, and 40 tiles of keys or more, on average
   const bool turns = static_cast<int64_t>(a.q_tokens) * a.group >= 2LL * kTile * a.batch &&
-                     a.kv_tokens >= 16LL * kTile * a.batch;
+                     a.kv_tokens >= 40LL * kTile * a.batch;
   cudaError_t e;
   if (a.dk <= 64 && a.dv <= 64)
     e = launch<1, 1>(a, q, k, v, grid, turns, stream);

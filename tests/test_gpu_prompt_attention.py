@@ -106,8 +106,9 @@ SHAPES = [  # query lengths, key lengths, heads, key heads, dk, dv
     ([2000], [2000], 2, 2, 128, 128),
     ([700], [5000], 1, 1, 192, 128),
     ([1], [40000], 2, 1, 192, 128),
-    ([300], [2100], 2, 2, 64, 64),
-    ([600, 300, 40], [2500, 5000, 40], 4, 1, 128, 128),
+    ([300], [5200], 2, 2, 64, 64),
+    ([600, 300, 40], [9000, 7000, 40], 4, 1, 128, 128),
+    ([700], [5300], 1, 1, 192, 128),
 ]
 
 
