@@ -457,18 +457,23 @@ bool plan(MatvecArgs* a, int nt, int tok_p) {
       if (blocks > a->n) blocks = a->n;
       int64_t rows = (a->n + blocks - 1) / blocks;
       if (rows > kMaxRows) rows = kMaxRows;
-      const int tiles = static_cast<int>((rows + 15) / 16);
       const int slice = (pieces + s - 1) / s;
       int most = a->x_codes ? (kSmemBytes / res - 2048 - pad) * 3 / 4 / per_piece : stage_tasks(nt) / tok_p;
       if (most < 1) continue;
       const int stage = slice < most ? slice : most;
+      // many rows and tokens: as many rows as leave their sums room beside a stage, in rounds
+      const int64_t room = kSmemBytes / res - (res > 1 ? 1024 : 0) - static_cast<int64_t>(stage) * per_piece - pad;
+      const int64_t fit = (room / (4 * tok_p) - 4) / 16 * 16;
+      if (fit < 16) continue;
+      if (rows > fit) rows = fit;
+      const int tiles = static_cast<int>((rows + 15) / 16);
       const int64_t rounds = ((a->n + rows - 1) / rows * s * others + sms * res - 1) / (sms * res);
       const int stages = (slice + stage - 1) / stage;
       const int lays = a->x_codes ? stages : (stage * tok_p + warps * 16 - 1) / (warps * 16) * stages;
       for (int bits = warp_bits(nt); bits >= 0; --bits) {
         const int wr = 1 << bits, wk = warps / wr;
         const int64_t smem = static_cast<int64_t>(stage) * per_piece + pad + sum_bytes(tok_p, wk, rows);
-        if (smem > kSmemBytes / res - (res > 1 ? 1024 : 0)) continue;
+        if (smem - static_cast<int64_t>(stage) * per_piece - pad > room) continue;
         const int share = (stage + wk - 1) / wk;
         const int64_t batches = static_cast<int64_t>(stages) * ((tiles + wr - 1) / wr) *
                                 ((share + batch(nt) - 1) / batch(nt));

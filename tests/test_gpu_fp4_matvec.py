@@ -174,3 +174,35 @@ def test_refusals():
         m.mla_fp4_matvec(b[..., :48], codes[..., :24].contiguous(), scales[..., :3].contiguous())
     with pytest.raises(m.MlaError):  # rows of out that overlap
         m.mla_fp4_matvec(b, codes, scales, out=torch.empty(64, device=DEV).as_strided((2, 1, 8), (4, 8, 1)))
+
+
+@pytest.mark.parametrize("kind,tokens,groups,n,k", [("bf16", 4096, 1, 1001, 16384), ("e4m3", 4096, 1, 1001, 25632),
+                                                    ("e4m3", 9, 300, 1048, 8192), ("bf16", 1, 4, 70000, 96)])
+def test_more_sums_than_fit_beside_the_tokens(kind, tokens, groups, n, k):
+    """Many rows of many tokens a CTA, or of many matrices: their sums leave the tokens
+    little room in shared memory, and CTAs come in rounds."""
+    m = lib()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    codes, scales = weights(g, groups, n, k)
+    x, xs = inputs(g, kind, tokens, groups, k)
+    y = m.mla_fp4_matvec(x, codes, scales, x_scales=xs, out_dtype=torch.float32)
+    for t in range(0, tokens, 1024):  # the comparison's memory
+        part = slice(t, t + 1024)
+        for j in range(0, groups, 30):
+            of = slice(j, j + 30)
+            check(y[part, of], x[part, of], None if xs is None else xs[part, of], codes[of], scales[of], None)
+
+
+def test_one_token_for_all_matrices():
+    """x with a stride of 0 over the groups."""
+    m = lib()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    codes, scales = weights(g, 5, 200, 352)
+    for kind in ("bf16", "e4m3"):
+        x, xs = inputs(g, kind, 3, 1, 352)
+        wide = x.expand(3, 5, 352)
+        xs = None if xs is None else xs.expand(3, 5, 3).contiguous()
+        y = m.mla_fp4_matvec(wide, codes, scales, x_scales=xs, out_dtype=torch.float32)
+        check(y, wide, xs, codes, scales, None)
