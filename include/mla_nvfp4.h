@@ -585,9 +585,12 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
  *                 read if kv_tokens is 0
  *   out           device bf16 [q_tokens, num_heads, v_dim]; tokens before the
  *                 first sequence and behind the last are not written
- *   strides       elements, multiples of 8; that of an axis with one entry is
- *                 not used; no two rows of out may share an element (checked).
- *                 All four tensors 16-byte aligned
+ *   strides       elements, multiples of 8, less than 2^39; that of an axis with
+ *                 one entry is not used; those of q, k and v at least qk_dim or
+ *                 v_dim (less, also the 0 of a repeated axis:
+ *                 MLA_ERR_UNSUPPORTED); no two rows of out may share an element
+ *                 (checked), out may not overlap an input.  All four tensors
+ *                 16-byte aligned
  *   query_start, kv_start   device int32 [batch + 1], not decreasing; values
  *                 outside [0, q_tokens] or [0, kv_tokens] are cut to it
  *   qk_dim        a multiple of 8, 8..192; v_dim 8..128 (more:
@@ -600,7 +603,8 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
  *                 256-byte aligned (that size depends on the current device
  *                 and may be 0); contents on entry do not matter; calls that
  *                 may run at the same time need one each
- * batch == 0 or q_tokens == 0 is a no-op.  At most 2^31 - 256 tokens.
+ * batch == 0 or q_tokens == 0 is a no-op.  At most 2^31 - 256 tokens, and
+ * q_tokens x num_heads < 2^31 (more: MLA_ERR_UNSUPPORTED).
  */
 size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
                                            int num_kv_heads, int v_dim);
@@ -673,7 +677,8 @@ mla_status_t mla_add_norm_quant(const uint16_t* x, int64_t x_stride, mla_residua
  *   weight_scale    device float [groups], or NULL: 1
  *   k               a multiple of 32 (odd multiples of 16: MLA_ERR_UNSUPPORTED)
  *   out             device bf16 or float, strides as x's, in elements (any);
- *                   no two rows may share an element (checked)
+ *                   no two rows may share an element (checked), nor may
+ *                   they overlap another argument
  *   groups          at most 65,535; n_tokens at most 2,097,120 (more:
  *                   MLA_ERR_UNSUPPORTED)
  * n_tokens, groups or n == 0 is a no-op.

@@ -870,8 +870,14 @@ mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int
   if ((q_tokens > 1 && (q_token_stride % 8 || out_token_stride % 8)) ||
       (num_heads > 1 && (q_head_stride % 8 || out_head_stride % 8)) ||
       (kv_tokens > 1 && (k_token_stride % 8 || v_token_stride % 8)) ||
-      (num_kv_heads > 1 && (k_head_stride % 8 || v_head_stride % 8)))
+      (kv_tokens > 0 && num_kv_heads > 1 && (k_head_stride % 8 || v_head_stride % 8)))
     return MLA_ERR_INVALID_ARG;
+  // rows that overlap, and so an axis repeated by a stride of 0, are nothing the copy engine's
+  // descriptions promise
+  if ((q_tokens > 1 && q_token_stride < qk_dim) || (num_heads > 1 && q_head_stride < qk_dim) ||
+      (kv_tokens > 1 && (k_token_stride < qk_dim || v_token_stride < v_dim)) ||
+      (kv_tokens > 0 && num_kv_heads > 1 && (k_head_stride < qk_dim || v_head_stride < v_dim)))
+    return MLA_ERR_UNSUPPORTED;
   if ((q_tokens > 1 && out_token_stride < v_dim) || (num_heads > 1 && out_head_stride < v_dim) ||
       rows_overlap(q_tokens, out_token_stride, num_heads, out_head_stride, v_dim))
     return MLA_ERR_INVALID_ARG;
@@ -904,7 +910,8 @@ mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int
   a.causal = causal != 0;
   a.negate = softmax_scale < 0.f;
   // a scale of 0 makes all weights equal, but must keep what is masked at -infinity
-  a.scale_log2 = std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 1.401298464324817e-45f);
+  // (and one past float's range, finite: a score of 0 stays 0)
+  a.scale_log2 = std::fmin(std::fmax(std::fabs(softmax_scale) * 1.4426950408889634f, 1.401298464324817e-45f), 3.402823466e38f);
   a.out = out;
   a.out_token = out_token_stride;
   a.out_head = out_head_stride;

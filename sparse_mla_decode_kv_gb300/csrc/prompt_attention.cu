@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
           if (here) {
-              if (direct) {
+            if (direct) {
               uint16_t* dst = args.out + t * args.out_token + head * args.out_head + c;
               uint32_t h[16];
 #pragma unroll
@@ -943,9 +943,10 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
   // a tensor without rows is described by one that is never read
   const uint64_t kv_rows = a.kv_tokens > 0 ? static_cast<uint64_t>(a.kv_tokens) : 1;
   const bool have = a.kv_tokens > 0;
+  const uint64_t kv_heads = have ? static_cast<uint64_t>(a.kv_heads) : 1;
   *described = encode_tensor_map_3d(&q, a.q, a.dk, a.heads, a.q_tokens, 2 * a.q_head, 2 * a.q_token, a.group, per) &&
-               encode_tensor_map_3d(&k, have ? a.k : a.q, a.dk, a.kv_heads, kv_rows, 2 * a.k_head, 2 * a.k_token, 1, kTile) &&
-               encode_tensor_map_3d(&v, have ? a.v : a.q, a.dv, a.kv_heads, kv_rows, 2 * a.v_head, 2 * a.v_token, 1, kTile);
+               encode_tensor_map_3d(&k, have ? a.k : a.q, a.dk, kv_heads, kv_rows, 2 * a.k_head, 2 * a.k_token, 1, kTile) &&
+               encode_tensor_map_3d(&v, have ? a.v : a.q, a.dv, kv_heads, kv_rows, 2 * a.v_head, 2 * a.v_token, 1, kTile);
   if (!*described) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(plan.places * a.kv_heads * a.splits);
   // both tiles filled, and 40 tiles of keys or more, on average

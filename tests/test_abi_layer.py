@@ -90,3 +90,15 @@ MATVEC = dict(x=FAKE, kind=0, xt=16 * 192, xg=192, xs=None, xsg=0, codes=FAKE, s
 ])
 def test_fp4_matvec(m, over, status):  # noqa: F811
     assert call(m, "mla_fp4_matvec", MATVEC, over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    *[({k: 0}, UNSUPPORTED) for k in ("qt", "qh", "kt", "kh", "vt", "vh")],  # an axis that is repeated
+    *[({k: 184}, UNSUPPORTED) for k in ("qt", "qh", "kt", "kh")], *[({k: 120}, UNSUPPORTED) for k in ("vt", "vh")],
+    *[({k: -1024}, UNSUPPORTED) for k in ("qt", "qh", "kt", "kh", "vt", "vh")],
+    # what is not used is not looked at
+    (dict(kv_heads=1, kh=0, vh=0, nq=2, nk=10 ** 6), TOO_SMALL), (dict(nk=1, kt=0, vt=0, kh=4), INVALID),
+    (dict(nk=1, kt=0, vt=0, kh=0), UNSUPPORTED),
+])
+def test_prompt_attention_strides(m, over, status):  # noqa: F811
+    assert call(m, "mla_prompt_attention", ATTENTION, over) == status

@@ -301,3 +301,37 @@ def test_refusals():
                     (10, 4, 64), (64, 64, 1)))):
         with pytest.raises(m.MlaError):
             bad()
+
+
+def test_no_keys_whatever_their_strides():
+    m = lib()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+    q = bf16(g, 5, 4, 64)
+    k = torch.empty((0, 1, 64), dtype=torch.bfloat16, device=DEV).expand(0, 2, 64)
+    lse = torch.zeros((5, 4), device=DEV)
+    out, _ = m.mla_prompt_attention(q, k, k, starts([2, 3]), starts([0, 0]), 0.1, lse=lse)
+    assert (out == 0).all() and lse.isneginf().all()
+
+
+def test_a_repeated_key_head_is_refused():
+    m = lib()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(10)
+    q, k = bf16(g, 7, 4, 64), bf16(g, 7, 1, 64)
+    with pytest.raises(m.MlaError):
+        m.mla_prompt_attention(q, k.expand(7, 4, 64), k.expand(7, 4, 64), starts([7]), starts([7]), 0.1)
+    out, _ = m.mla_prompt_attention(q, k, k, starts([7]), starts([7]), 0.1)  # one key head for all
+    check(out, None, q, k, k, [0, 7], [0, 7], 0.1, True)
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_the_largest_scales(scale):
+    """Scores 0 and of the order of the scale: all weight lies on the largest."""
+    m = lib()
+    q = torch.ones((1, 1, 64), dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros((3, 1, 64), dtype=torch.bfloat16, device=DEV)
+    k[1, 0, 0] = -2.0 ** -10 if scale > 0 else 2.0 ** -10
+    v = torch.tensor([1.0, 100.0, 3.0], device=DEV)[:, None, None].expand(3, 1, 64).to(torch.bfloat16).contiguous()
+    out, _ = m.mla_prompt_attention(q, k, v, starts([1]), starts([3]), scale)
+    assert (out == 2.0).all()
