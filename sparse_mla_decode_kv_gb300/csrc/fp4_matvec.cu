@@ -435,7 +435,8 @@ cudaError_t launch(const MatvecArgs& a, cudaStream_t stream) {
 // warp's batches (`wait` each), the rounds in which the tokens are laid out, and
 // what a cluster costs.  Clusters do not find a place on every SM (a group of SMs
 // that share one has 18 to 20): a grid for all 152 ran in two rounds, so one SM in
-// 19 is left out.  Measured, the chosen one first (row warps, splits, CTAs an SM): one
+// 19 is left out, and 5 in 19 where 8 CTAs have an SM each (32 bf16 tokens x 6144 x 6144
+// 35.6 us with 18 such clusters, 22.1 with 14; 20.6 with 36 of 4).  Measured, the chosen one first (row warps, splits, CTAs an SM): one
 // token x 12288 x 6144 14.5 us with 2, 1, 3, then 15.8 (4, 2, 3), 16.6 (1, 1, 3); 32 x
 // 6144 x 12288 29.7 with 16, 4, 1, then 33.8 (8, 2, 1), 42 (8, 1, 1); 8 x 8192 x 8192
 // 18.6 with 8, 4, 3, then 20.2 (2, 2, 2), 21.9 (1, 1, 3).
@@ -450,8 +451,8 @@ bool plan(MatvecArgs* a, int nt, int tok_p) {
   const int64_t others = static_cast<int64_t>(a->groups) * ((a->tokens + 8 * nt - 1) / (8 * nt));
   int64_t best = -1;
   for (int s = 1; s <= kMaxSplits && s <= pieces; s *= 2) {
-    const int64_t sms = s == 1 ? all_sms : all_sms * 18 / 19;
     for (int res = resident(nt); res >= 1; --res) {
+      const int64_t sms = s == 1 ? all_sms : all_sms * (s == 8 && res == 1 ? 14 : 18) / 19;
       int64_t blocks = sms * res / (s * others);
       if (blocks < 1) blocks = 1;
       if (blocks > a->n) blocks = a->n;
