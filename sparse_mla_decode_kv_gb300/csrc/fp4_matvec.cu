@@ -25,9 +25,11 @@
 // Bound: HBM, 9/16 byte a weight, and for these matrices the unpacking before it.
 // 16 rows x 128 values take a warp 107 instructions with up to 8 tokens, 64 cycles of
 // an SM: 4.6 to 4.8 TB/s where memory gives 6.8 (without the scales' multiplications
-// 5.8), plus 4 us of start and end.  One token x 12288 x 6144 14.4 us, 2,950 GB/s; four
-// x 24583 x 6144 27.3 us, 3,130.  With 32 tokens it is 290 instructions and 170 cycles
-// (the tokens' conversion, the products): x 6144 x 12288 29.6 us.
+// 5.8), plus 4 us of start and end.  One token x 12288 x 6144 14.4 us, 2,950 GB/s; x
+// 128,000 x 6144 94 us, 4,700; four x 24583 x 6144 25.4 us, 3,360.  With 32 tokens it is
+// 290 instructions and 150 cycles (the tokens' conversion, the products): x 6144 x 12288
+// 28.8 us.  Weights that were started on their way to L2 as a whole before the tokens
+// were laid out gained nothing any more: 14.5, 107, 27.0, 27.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -83,10 +85,6 @@ __device__ __forceinline__ uint32_t load_two(const uint8_t* p) {
   asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
-// Starts bringing memory to L2 (both 16-byte aligned).
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 // The first product of a sum: nothing to add to.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -126,19 +124,6 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
   auto share_n = [&](int s) { return ((stage_n(s) * (w_k + 1)) >> wk_bits) - share_lo(s); };
   const int64_t code_row = a.k / 2, scale_row = a.k / 16;
 
-  // The CTA's weights are on their way to L2 while the tokens are awaited and laid out,
-  // also while the kernel in front still runs (who writes them after that writes to L2).
-  // Whole rows of k alone, and scales where they begin at multiples of 16 bytes.
-  if (p_lo < p_hi) {
-    const int64_t k0 = static_cast<int64_t>(p_lo) * kPiece;
-    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(p_hi) * kPiece, static_cast<int64_t>(a.k)) - k0) / 2;
-    const bool with_scales = a.k % 256 == 0 && p_lo % 2 == 0 && p_hi % 2 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0;
-    for (int r = threadIdx.x; r < rows_cta; r += kThreads) {
-      const int64_t row = static_cast<int64_t>(grp) * a.n + row0 + r;
-      prefetch_l2(a.codes + row * code_row + k0 / 2, bytes);
-      if (with_scales) prefetch_l2(a.scales + row * scale_row + k0 / 16, bytes / 8);
-    }
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -370,6 +355,14 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
   }
 
   // ---- sums of the warps along k, then of the cluster's CTAs, each in its order
+  if (wk > 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < toks * pitch; i += kThreads) {
+      float y = s_sum[i];
+      for (int k = 1; k < wk; ++k) y += s_sum[k * tok_p * pitch + i];
+      s_sum[i] = y;
+    }
+  }
   if (a.splits > 1)
     cluster_sync_all();
   else
@@ -379,18 +372,17 @@ __global__ void __launch_bounds__(32 << warp_bits(NT), resident(NT)) fp4_matvec_
   const int r_lo = min(split * each, rows_cta), r_n = min(each, rows_cta - r_lo);
   for (int i = threadIdx.x; i < r_n * toks; i += kThreads) {
     const int tok = i / r_n, r = r_lo + (i - tok * r_n);
-    float y = 0.f;
-    for (int k = 0; k < wk; ++k) {
-      const float* p = s_sum + (k * tok_p + tok) * pitch + r;
-      if (a.splits > 1) {
-        float v[kMaxSplits];
+    const float* const p = s_sum + tok * pitch + r;
+    float y;
+    if (a.splits > 1) {
+      float v[kMaxSplits];
 #pragma unroll
-        for (int c = 0; c < kMaxSplits; ++c) v[c] = c < a.splits ? cluster_read(p, c) : 0.f;
+      for (int c = 0; c < kMaxSplits; ++c) v[c] = c < a.splits ? cluster_read(p, c) : 0.f;
+      y = v[0];
 #pragma unroll
-        for (int c = 0; c < kMaxSplits; ++c) y += v[c];
-      } else {
-        y += *p;
-      }
+      for (int c = 1; c < kMaxSplits; ++c) y += v[c];
+    } else {
+      y = *p;
     }
     y *= factor;
     const int64_t at = (tok0 + tok) * a.out_token + grp * a.out_group + row0 + r;
