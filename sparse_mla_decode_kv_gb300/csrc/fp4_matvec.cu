@@ -428,10 +428,11 @@ cudaError_t launch(const MatvecArgs& a, cudaStream_t stream) {
 // what a cluster costs.  Clusters do not find a place on every SM (a group of SMs
 // that share one has 18 to 20): a grid for all 152 ran in two rounds, so one SM in
 // 19 is left out, and 5 in 19 where 8 CTAs have an SM each (32 bf16 tokens x 6144 x 6144
-// 35.6 us with 18 such clusters, 22.1 with 14; 20.6 with 36 of 4).  Measured, the chosen one first (row warps, splits, CTAs an SM): one
-// token x 12288 x 6144 14.5 us with 2, 1, 3, then 15.8 (4, 2, 3), 16.6 (1, 1, 3); 32 x
-// 6144 x 12288 29.7 with 16, 4, 1, then 33.8 (8, 2, 1), 42 (8, 1, 1); 8 x 8192 x 8192
-// 18.6 with 8, 4, 3, then 20.2 (2, 2, 2), 21.9 (1, 1, 3).
+// 35.6 us with 18 such clusters, 20.5 with 14).  Measured, the chosen one first (row
+// warps, splits, CTAs an SM): one token x 12288 x 6144 14.5 us with 2, 1, 3, then 14.7
+// (8, 4, 3), 15.1 (4, 2, 3), 16.4 (1, 1, 3); 32 x 6144 x 12288 28.8 with 4, 4, 1, then 29.5
+// (16, 4, 1), 31.7 (16, 8, 1), 35.0 (8, 2, 1); 8 x 8192 x 8192 19.2 with 2, 4, 3, where
+// 8, 4, 3 takes 18.0.
 bool plan(MatvecArgs* a, int nt, int tok_p) {
   const int per_piece = a->x_codes ? raw_piece_bytes(tok_p) : piece_bytes(nt, tok_p);
   const int pad = a->x_codes ? tok_p * kRawPad : 0;
