@@ -21,8 +21,10 @@
 // copies, one looks through the values that some row must not see, and two groups
 // of four warps have a tile's softmax, a thread a row: maximum and sum stay in
 // registers.  A tile's products have one issuing thread and complete in order, so a
-// full S says that the product before it, which read P and V, is done too.  Slices'
-// partial outputs are joined by their LSEs in a second kernel.
+// full S says that the product before it, which read P and V, is done too.  Where
+// a sequence has rows for one tile only, the second tile is the same rows again with
+// every other tile of keys, joined in the CTA at the end.  Slices' partial outputs are
+// joined by their LSEs in a second kernel.
 //
 // What bounds it.  Over many keys power (1,380 of 1,400 W) and the chain score,
 // softmax, product of each tile, which the other tile's hides in part: 16,384 tokens
@@ -31,7 +33,8 @@
 // The same with one CTA a unit 163, units taken in turn 156, a product warp a tile
 // and maxima from the loads 144, exponentials in turn 134.  Short prompts (16 packed
 // ones of up to 1,500 tokens, 160 us) pay each unit's last softmax and output, 3 to 4
-// us; single tokens walk memory: one over 100,000 keys x 16 heads 163 us, 6,250 GB/s.
+// us; single tokens walk memory: 32 over up to 8,192 keys x 64 / 8 heads 115 us, 5,450
+// GB/s (124 with their tiles of keys one after the other); one over 8,192 x 32 / 8 17.
 //
 // Values that a row must not see.  A weight of 0 does not keep an infinity or
 // NaN out of a product.  Where some row's mask cuts a tile of keys, its values are
@@ -62,7 +65,7 @@ constexpr int kChunkBytes = kTile * 128;  // 128 rows of 64 values
 constexpr int kItems = 16;                // barriers of copied tiles (keys and values in turn)
 constexpr int kUnits = 2;                 // units that are known: one in work, one ahead
 constexpr int kSmemBytes = 227 * 1024;
-constexpr int kCtlBytes = 1024;
+constexpr int kCtlBytes = 2048;
 constexpr uint32_t kSCol = 0, kOCol = 256, kTmemCols = 512;
 constexpr int kTurnPolls = 40;  // of about 30 cycles
 constexpr int64_t kMaxSlice = 65536;  // tiles of keys
@@ -86,6 +89,8 @@ struct Unit {
   int split;
   int begin;
   int count[2];
+  int steps;   // tiles of keys that are copied
+  int paired;  // tile 1 has tile 0's rows, and every other one of its tiles of keys
   int first_masked;  // tiles of keys from this one on are not seen in full by some row
   int last;          // nothing comes any more
 };
@@ -102,6 +107,8 @@ struct Ctl {
   uint32_t bad[kUnits][kMaskedTiles][kTile / 32];  // keys of the masked tiles that held an infinity or NaN
   int any_bad[kUnits];
   int busy[2][4];  // a softmax warp is at its exponentials
+  uint64_t half_full, half_free;  // the second half of a paired tile: in tensor memory and here, read
+  float half_ref[kTile], half_sum[kTile];
 };
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
@@ -268,7 +275,7 @@ __device__ __forceinline__ int visible(const PromptArgs& a, int nq, int nk, int 
 // Unit `id`, found by a whole warp; false if it is empty.  Sequence b's pairs of tiles
 // have the places from q_start[b] / tokens + b on: as many as there are places before
 // sequence b + 1's, or fewer.
-__device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane, Unit& u) {
+__device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane, bool pairs, Unit& u) {
   const int per = kTile / a.group;  // tokens of a tile
   u.split = id % a.splits;
   const int rest = id / a.splits;
@@ -302,12 +309,20 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane,
   const int end = static_cast<int>(all * (u.split + 1) / a.splits);
 #pragma unroll
   for (int s = 0; s < 2; ++s) u.count[s] = max(0, min(end, n[s]) - u.begin);
+  u.steps = max(u.count[0], u.count[1]);
+  u.paired = pairs && u.tok + per >= u.nq && u.steps > 1;
+  if (u.paired) {
+    u.count[0] = (u.steps + 1) / 2;
+    u.count[1] = u.steps / 2;
+  }
   u.first_masked = visible(a, u.nq, u.nk, u.tok) / kTile;
   return true;
 }
 
-// kTurns: the two tiles' exponentials take turns, see there.
-template <int KC, int VC, bool kTurns>
+// kTurns: the two tiles' exponentials take turns, see there.  kPairs: where a sequence's rows
+// fill one tile at most, the other one has the same rows and every second tile of keys.
+enum Mode { kPlain, kTurns, kPairs };
+template <int KC, int VC, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const PromptArgs args, const __grid_constant__ CUtensorMap q_map,
                             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -345,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems / 2; ++i) mbar_init(&sm.ready[i], 1);
     mbar_init(&sm.canceled, 1);
+    mbar_init(&sm.half_full, 4);
+    mbar_init(&sm.half_free, 4);
     sm.abort_flag = 0;
     for (int i = 0; i < 8; ++i) sm.busy[i >> 2][i & 3] = 0;
     fence_mbar_init();
@@ -380,22 +397,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (uint32_t asked = 0; ok && id >= 0; ++asked) {
         Unit u;
-        if (find_unit(args, id, lane, u)) {
+        if (find_unit(args, id, lane, kMode == kPairs, u)) {
           if (n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
           if (ok && leader) {
             sm.unit[n % kUnits] = u;
             sm.any_bad[n % kUnits] = 0;
             for (int i = 0; i < kMaskedTiles * (kTile / 32); ++i) sm.bad[n % kUnits][0][i] = 0;
             mbar_arrive(&sm.unit_full[n % kUnits]);
-            const int items = 2 * max(u.count[0], u.count[1]);
+            const int items = 2 * (kMode == kPairs ? u.steps : max(u.count[0], u.count[1]));
             auto copy_q = [&](int s) {
               if (q_uses[s] > 0) ok = wait_bar(sm, &sm.q_free[s], (q_uses[s] - 1) & 1u, fw);
               if (!ok) return;
               mbar_expect_tx(&sm.q_full[s], static_cast<uint32_t>(KC * rows * 128));
               ++q_uses[s];
               for (int c = 0; c < KC; ++c)
-                tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, u.head * args.group, u.q0 + u.tok + s * per,
-                            &sm.q_full[s]);
+                tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, u.head * args.group,
+                            u.q0 + u.tok + (kMode == kPairs && u.paired ? 0 : s * per), &sm.q_full[s]);
             };
             for (int i = 0; i < items && ok; ++i) {
               const int chunks = (i & 1) ? VC : KC;
@@ -471,7 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
           if (!ok || sm.unit[n % kUnits].last) break;
           const int count = s == 0 ? sm.unit[n % kUnits].count[0] : sm.unit[n % kUnits].count[1];
-          const int n_tiles = max(count, s == 0 ? sm.unit[n % kUnits].count[1] : sm.unit[n % kUnits].count[0]);
+          const int n_tiles = kMode == kPairs ? sm.unit[n % kUnits].steps
+                                              : max(count, s == 0 ? sm.unit[n % kUnits].count[1] : sm.unit[n % kUnits].count[0]);
+          // of a paired unit's tiles of keys every other one is this tile's
+          const bool paired = kMode == kPairs && sm.unit[n % kUnits].paired;
+          auto ours = [&](int j) { return paired ? (j & 1) == s : j < count; };
+          auto nth = [&](int j) { return paired ? j >> 1 : j; };
           mbar_arrive(&sm.unit_free[n % kUnits]);
           if (n_tiles == 0) continue;
           auto scores = [&](int j, int k_at) {  // S of keys j, which begin at chunk k_at
@@ -484,13 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_ss(d_s, q_desc + ((c * kChunkBytes + 32 * i) >> 4), k_desc + (32 * i >> 4), idesc_s, c > 0 || i > 0);
             }
             umma_commit(&sm.s_full[s]);
-            if (j + 1 == count) umma_commit(&sm.q_free[s]);
+            if (nth(j) + 1 == count) umma_commit(&sm.q_free[s]);
           };
           ok = wait_bar(sm, &sm.full[item % kItems], parity(item), fw);
           if (ok && count > 0) {
             ok = wait_bar(sm, &sm.q_full[s], q_uses & 1u, fw);
             ++q_uses;
-            if (ok) {
+            if (ok && ours(0)) {
               tcgen05_fence_after();
               scores(0, at);
             }
@@ -503,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             v_at = v_at >= kRing ? v_at - kRing : v_at;
             k_at = k_at >= kRing ? k_at - kRing : k_at;
             ok = wait_bar(sm, &sm.ready[v_item / 2 % (kItems / 2)], parity(v_item), fw);
-            if (ok && j < count) {
+            if (ok && ours(j)) {
               // the product of the first half of the keys runs while the other's weights
               // are computed
 #pragma unroll
@@ -517,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint64_t v_desc = desc_values(v0);
 #pragma unroll
                   for (int i = 4 * half; i < 4 * half + 4; ++i)
-                    umma_ts(d_o, d_s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, j > 0 || i > 0);
+                    umma_ts(d_o, d_s + 8 * i, v_desc + (2048 * i >> 4), idesc_o, nth(j) > 0 || i > 0);
                 } else {
 #pragma unroll
                   for (int c = 0; c < VC; ++c) {
@@ -525,17 +547,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 4 * half; i < 4 * half + 4; ++i)
                       umma_ts(d_o + 64 * c, d_s + 8 * i, v_desc + (2048 * i >> 4), bf16_idesc(64, false, true),
-                              j > 0 || i > 0);
+                              nth(j) > 0 || i > 0);
                   }
                 }
               }
               ++p_uses;
-              if (ok && j + 1 == count) umma_commit(&sm.o_full[s]);
+              if (ok && nth(j) + 1 == count) umma_commit(&sm.o_full[s]);
             }
             umma_commit(&sm.free_[v_item % kItems]);
             if (ok && j + 1 < n_tiles) {
               ok = wait_bar(sm, &sm.full[k_item % kItems], parity(k_item), fw);
-              if (ok && j + 1 < count) scores(j + 1, k_at);
+              if (ok && ours(j + 1)) scores(j + 1, k_at);
               umma_commit(&sm.free_[k_item % kItems]);
             }
             item += 2;
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar_warp(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
         if (!ok || sm.unit[n % kUnits].last) break;
         const Unit& u = sm.unit[n % kUnits];
-        const int n_tiles = max(u.count[0], u.count[1]);
+        const int n_tiles = kMode == kPairs ? u.steps : max(u.count[0], u.count[1]);
         const int masked0 = u.first_masked - u.begin;  // tiles from this one on
         const int seen = visible(args, u.nq, u.nk, u.tok);  // keys before it are seen by all rows
         for (int j = 0; j < n_tiles && ok; ++j) {
@@ -616,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lanes + kSCol + kTile * s, o_addr = lanes + kOCol + kTile * s;
     const float sl = args.scale_log2;
     const uint64_t sl2 = pack2(sl, sl);
-    uint32_t s_uses = 0, o_uses = 0;
+    uint32_t s_uses = 0, o_uses = 0, pairs = 0;
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
@@ -624,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || sm.unit[n % kUnits].last) break;
       const Unit& u = sm.unit[n % kUnits];
       const int count = s == 0 ? u.count[0] : u.count[1];
-      const int tok0 = u.tok + s * per, tok = tok0 + row_tok;
+      const bool paired = kMode == kPairs && u.paired;
+      const int tok0 = u.tok + (paired ? 0 : s * per), tok = tok0 + row_tok;
       const int head = u.head * args.group + row_head;
       const bool here = row < rows && tok < u.nq;
       const int lim = here ? visible(args, u.nq, u.nk, tok) : 0;
@@ -644,8 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld64_max(s_addr + 64, z[1], most[1]);
         tmem_wait(z[0], most[0]);
         tmem_wait(z[1], most[1]);
-        if (begin + j >= tile_full) {
-          const int rel = lim - (begin + j) * kTile;
+        const int at_key = begin + (paired ? 2 * j + s : j);  // tile of keys
+        if (at_key >= tile_full) {
+          const int rel = lim - at_key * kTile;
           most[0] = most[1] = -INFINITY;
 #pragma unroll
           for (int i = 0; i < kTile; ++i) {
@@ -680,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // waited long enough goes on.  It pays over many tiles of keys (x 16 heads, with
         // and without): 16,384 tokens of 192 dims 805 and 868 us, of 128 693 and 767, 6,000
         // of 192 134 and 142; 2 x 4,096 of 128 124 and 118, 2 x 3,000 of 192 91 and 85.
-        if (kTurns) {
+        if (kMode == kTurns) {
           for (int i = 0; i < kTurnPolls && *reinterpret_cast<volatile int*>(&sm.busy[s ^ 1][quad]) != 0; ++i) {
           }
           if (lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 1;
@@ -710,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part == 2) publish(0);
           tmem_st16(s_addr + 16 * part, p);
         }
-        if (kTurns && lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 0;
+        if (kMode == kTurns && lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 0;
         publish(1);
       }
       // ---- output
@@ -725,7 +749,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar_warp(sm, &sm.o_full[s], o_uses & 1u, fw);
         ++o_uses;
       }
-      if (ok && tok0 < u.nq) {
+      // A paired tile's halves are joined as slices are: the second one's group leaves its
+      // maximum and sum, the first one's reads both sums of values.
+      float mine = 1.f, others = 0.f;  // weights of the halves
+      if (paired) {
+        if (s == 1) {
+          sm.half_ref[row] = ref;
+          sm.half_sum[row] = l;
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.half_full);
+          if (ok) ok = wait_bar_warp(sm, &sm.half_free, pairs & 1u, fw);
+        } else if (ok) {
+          ok = wait_bar_warp(sm, &sm.half_full, pairs & 1u, fw);
+          const float ref2 = sm.half_ref[row], most = fmaxf(ref, ref2);
+          mine = ref == -INFINITY ? 0.f : ex2(ref - most);
+          others = ref2 == -INFINITY ? 0.f : ex2(ref2 - most);
+          l = mine * l + others * sm.half_sum[row];  // a NaN in either (no score was a number) stays
+          ref = most;
+        }
+        ++pairs;
+      }
+      if (ok && tok0 < u.nq && !(paired && s == 1)) {
         tcgen05_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t t = u.q0 + tok;
@@ -742,7 +787,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < args.dv; c += 32) {
           uint32_t o[32];
-          if (count > 0) {
+          if (paired) {
+            uint32_t o2[32];
+            tmem_load_32cols(o_addr + c, o);
+            tmem_load_32cols(o_addr + kTile + c, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = mine == 0.f ? 0.f : mine * __uint_as_float(o[i]);
+              o[i] = __float_as_uint(others == 0.f ? x : fmaf(others, __uint_as_float(o2[i]), x));
+            }
+          } else if (count > 0) {
             tmem_load_32cols(o_addr + c, o);
           } else {
 #pragma unroll
@@ -804,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the tensor memory has been read, by this unit's last loads or its next ones' wait
       tcgen05_fence_before();
       __syncwarp();
+      if (paired && s == 0 && lane == 0) mbar_arrive(&sm.half_free);
       if (lane == 0) mbar_arrive(&sm.unit_free[n % kUnits]);
     }
   }
@@ -907,11 +962,12 @@ cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, 
 
 template <int KC, int VC>
 cudaError_t launch(PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, unsigned grid,
-                   bool turns, cudaStream_t stream) {
-  const void* kernel = turns ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, true>)
-                             : reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, false>);
-  static std::atomic<uint64_t> configured[2];
-  const cudaError_t e = set_smem_limit_once(kernel, kSmemBytes, &configured[turns ? 1 : 0]);
+                   Mode mode, cudaStream_t stream) {
+  const void* kernel = mode == kTurns   ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kTurns>)
+                       : mode == kPairs ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPairs>)
+                                        : reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPlain>);
+  static std::atomic<uint64_t> configured[3];
+  const cudaError_t e = set_smem_limit_once(kernel, kSmemBytes, &configured[mode]);
   if (e != cudaSuccess) return e;
   void* params[] = {&a, const_cast<CUtensorMap*>(&q), const_cast<CUtensorMap*>(&k), const_cast<CUtensorMap*>(&v)};
   return launch_dependent(kernel, grid, kThreads, kSmemBytes, params, stream);
@@ -985,16 +1041,20 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
                encode_tensor_map_3d(&v, have ? a.v : a.q, a.dv, kv_heads, kv_rows, 2 * a.v_head, 2 * a.v_token, 1, kTile);
   if (!*described) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(plan.places * a.kv_heads * a.splits);
-  // both tiles filled, and 40 tiles of keys or more, on average
-  const bool turns = static_cast<int64_t>(a.q_tokens) * a.group >= 2LL * kTile * a.batch &&
-                     a.kv_tokens >= 40LL * kTile * a.batch;
+  // turns: both tiles filled, and 40 tiles of keys or more, on average; pairs: at most one tile
+  // filled, and more than one tile of keys (32 single tokens over up to 8,192 keys x 64 / 8
+  // heads 114.8 us, 123.9 without; where no unit is paired they cost 3 %)
+  const int64_t rows = static_cast<int64_t>(a.q_tokens) * a.group, keys = a.kv_tokens;
+  const Mode mode = rows >= 2LL * kTile * a.batch && keys >= 40LL * kTile * a.batch ? kTurns
+                    : rows <= 1LL * kTile * a.batch && keys > 1LL * kTile * a.batch * a.splits ? kPairs
+                                                                                              : kPlain;
   cudaError_t e;
   if (a.dk <= 64 && a.dv <= 64)
-    e = launch<1, 1>(a, q, k, v, grid, turns, stream);
+    e = launch<1, 1>(a, q, k, v, grid, mode, stream);
   else if (a.dk <= 128)
-    e = launch<2, 2>(a, q, k, v, grid, turns, stream);
+    e = launch<2, 2>(a, q, k, v, grid, mode, stream);
   else
-    e = launch<3, 2>(a, q, k, v, grid, turns, stream);
+    e = launch<3, 2>(a, q, k, v, grid, mode, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t pairs = static_cast<int64_t>(a.q_tokens) * a.heads;
   void* merge[] = {&a};

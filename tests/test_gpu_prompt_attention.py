@@ -335,3 +335,29 @@ def test_the_largest_scales(scale):
     v = torch.tensor([1.0, 100.0, 3.0], device=DEV)[:, None, None].expand(3, 1, 64).to(torch.bfloat16).contiguous()
     out, _ = m.mla_prompt_attention(q, k, v, starts([1]), starts([3]), scale)
     assert (out == 2.0).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", [
+    ([300, 1, 1, 1], [500, 3000, 700, 129], 2, 2, 128, 128),
+    ([1, 140, 2], [4000, 4100, 257], 1, 1, 192, 128),
+    ([2, 3, 1, 0, 4], [257, 128, 129, 500, 0], 8, 2, 64, 64),
+    ([9, 7], [1290, 3], 12, 1, 96, 80),
+    ([128, 128], [1000, 385], 1, 1, 64, 64),
+])
+def test_few_rows_over_many_keys(shape, causal):
+    """One tile of rows for most sequences, whose tiles of keys two groups share; others with
+    more rows, one tile of keys or none in the same call."""
+    m = lib()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(11)
+    q, k, v, qs, ks, scale, out, lse = run(m, g, *shape, causal=causal)
+    again, _ = m.mla_prompt_attention(q, k, v, qs, ks, scale, causal=causal)
+    assert torch.equal(again, out)
+    # scores that grow along the keys, and ones that fall: either half has the largest
+    for sign in (1, -1):
+        k2 = (k.float() * 0.1 + sign * torch.linspace(-1, 1, k.shape[0], device=DEV)[:, None, None]).to(torch.bfloat16)
+        q2 = (q.float() * 0.1 + 1).to(torch.bfloat16)
+        lse = torch.empty_like(lse)
+        out, _ = m.mla_prompt_attention(q2, k2, v, qs, ks, 0.7, causal=causal, lse=lse)
+        check(out, lse, q2, k2, v, qs.tolist(), ks.tolist(), 0.7, causal)
