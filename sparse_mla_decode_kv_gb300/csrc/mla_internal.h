@@ -185,7 +185,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 
 // Attention over packed prompts (prompt_attention.cu).
 struct PromptPlan {
-  int64_t places;    // of pairs of row tiles, per key head
+  int64_t places;    // of units, per key head
+  int unit_tiles;    // tiles of rows in a unit: 1 or 2
   int splits;        // CTAs per pair along the keys
   size_t workspace;  // bytes of partials, 0 for a single slice
 };
@@ -206,7 +207,7 @@ struct PromptArgs {
   int64_t out_token, out_head;
   float* lse;  // [q_tokens, heads] or null
   // set by the launch from the plan
-  int group, splits, places;
+  int group, splits, places, unit_tiles;
   bool out_wide;  // rows of out begin and end at multiples of 32 bytes
   float* part_o;
   float* part_lse;

@@ -277,11 +277,12 @@ __device__ __forceinline__ int visible(const PromptArgs& a, int nq, int nk, int 
 // sequence b + 1's, or fewer.
 __device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane, bool pairs, Unit& u) {
   const int per = kTile / a.group;  // tokens of a tile
+  const int span = pairs ? a.unit_tiles * per : 2 * per;  // and of a unit
   u.split = id % a.splits;
   const int rest = id / a.splits;
   u.head = rest % a.kv_heads;
   const int place = a.places - 1 - rest / a.kv_heads;  // the longest rows of a sequence first
-  auto first_place = [&](int b) { return min(max(a.q_start[b], 0), a.q_tokens) / (2 * per) + b; };
+  auto first_place = [&](int b) { return min(max(a.q_start[b], 0), a.q_tokens) / span + b; };
   int lo = -1, hi = a.batch;  // the last b in [lo, hi) whose first place is not behind this one
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -295,14 +296,14 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane,
   u.nq = max(0, min(max(a.q_start[lo + 1], 0), a.q_tokens) - u.q0);
   u.k0 = min(max(a.kv_start[lo], 0), a.kv_tokens);
   u.nk = max(0, min(max(a.kv_start[lo + 1], 0), a.kv_tokens) - u.k0);
-  u.tok = (place - (u.q0 / (2 * per) + lo)) * 2 * per;
+  u.tok = (place - (u.q0 / span + lo)) * span;
   u.last = 0;
   if (u.tok < 0 || u.tok >= u.nq) return false;
   int n[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int t = u.tok + s * per;
-    n[s] = t < u.nq ? (visible(a, u.nq, u.nk, min(t + per, u.nq) - 1) + kTile - 1) / kTile : 0;
+    n[s] = t < u.nq && s * per < span ? (visible(a, u.nq, u.nk, min(t + per, u.nq) - 1) + kTile - 1) / kTile : 0;
   }
   const int64_t all = max(n[0], n[1]);
   u.begin = static_cast<int>(all * u.split / a.splits);
@@ -310,7 +311,7 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane,
 #pragma unroll
   for (int s = 0; s < 2; ++s) u.count[s] = max(0, min(end, n[s]) - u.begin);
   u.steps = max(u.count[0], u.count[1]);
-  u.paired = pairs && u.tok + per >= u.nq && u.steps > 1;
+  u.paired = pairs && (span == per || (u.tok + per >= u.nq && u.steps > 1));
   if (u.paired) {
     u.count[0] = (u.steps + 1) / 2;
     u.count[1] = u.steps / 2;
@@ -975,37 +976,50 @@ cudaError_t launch(PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, co
 
 }  // namespace
 
-// How the keys are split: modelled time in tiles of keys.  Up to a unit an SM, a
-// slice and a start worth three; else the SMs' share of all slices and starts, and
-// a slice at the end, when others have run out.  The partials' joining is a launch
-// worth two tiles and their bytes (a tile takes about 1.7 us, in which memory
-// writes and reads 10 MB).  Lengths are known on the device only: every sequence is
-// taken for an equal share of the tokens.
+// How many tiles of rows a unit has, and how its keys are split: modelled time in tiles
+// of keys.  Up to a unit an SM, a slice (half of one and the halves' joining where both
+// tiles have the same rows) and a start worth three; else the SMs' share of all slices
+// and starts, and a slice at the end, when others have run out.  The partials' joining is
+// a launch worth two tiles and their bytes (a tile takes about 1.7 us, in which memory
+// writes and reads 10 MB).  Units of one tile leave fewer SMs idle: 7 x 33 tokens x 28 / 4
+// heads over 315 keys 11.3 us (13.2 with two), 3 x 200 x 4 / 2 over 6,000 21.3 (23.9).
+// Lengths are known on the device only: every sequence is taken for an equal share of
+// the tokens.
 PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch, int heads, int kv_heads, int dv) {
   PromptPlan p{};
   const int group = heads / kv_heads;
   const int64_t per = kTile / group;
-  p.places = q_tokens / (2 * per) + batch;
-  const int64_t used = ((q_tokens + batch - 1) / batch + 2 * per - 1) / (2 * per) * batch;  // places of equal shares
-  const int64_t units = (used < p.places ? used : p.places) * kv_heads;
-  // unequal shares may need a place more each: a second round would cost as much as the first
-  // (2 sequences of up to 300 tokens x 8 heads over up to 2,000 keys: 7 slices 26.2 us, 6 21.6)
-  const int64_t most = batch == 1 ? units : p.places * kv_heads;
   const int64_t sms = device_sm_count();
   const int64_t tiles = (kv_tokens / batch + kTile - 1) / kTile;
+  const int64_t share = (q_tokens + batch - 1) / batch;  // tokens of a sequence
   const double rows_mb = static_cast<double>(q_tokens) * heads * (dv + 1) * 8e-6;  // of one slice, written and read
   double best = -1;
   p.splits = 1;
-  for (int64_t n = 1; n <= (tiles > 1 ? tiles : 1) && n <= sms; ++n) {
-    const double slice = static_cast<double>((tiles + n - 1) / n);
-    double cost = slice + 3;
-    if (most * n > sms) cost = static_cast<double>(units * (tiles + 3 * n)) / static_cast<double>(sms) + slice;
-    if (n > 1) cost += 2 + rows_mb * static_cast<double>(n) * 0.1;
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.splits = static_cast<int>(n);
+  for (int unit = 2; unit >= 1; --unit) {  // tiles of rows
+    const int64_t places = q_tokens / (unit * per) + batch;
+    const int64_t used = (share + unit * per - 1) / (unit * per) * batch;  // of equal shares
+    const int64_t units = (used < places ? used : places) * kv_heads;
+    // unequal shares may need a place more each: a second round would cost as much as the first
+    // (2 sequences of up to 300 tokens x 8 heads over up to 2,000 keys: 7 slices 26.2 us, 6 21.6)
+    const int64_t most = batch == 1 ? units : places * kv_heads;
+    const bool paired = share <= per;
+    for (int64_t n = 1; n <= (tiles > 1 ? tiles : 1) && n <= sms; ++n) {
+      const int64_t slice = (tiles + n - 1) / n;
+      double cost = static_cast<double>(slice) + 3;
+      if ((unit == 1 || paired) && slice > 1) cost = static_cast<double>((slice + 1) / 2) + 3.5;
+      if (most * n > sms) {
+        if (unit == 1) break;  // more units than SMs: the keys are read for two tiles at once
+        cost = static_cast<double>(units * (tiles + 3 * n)) / static_cast<double>(sms) + static_cast<double>(slice);
+      }
+      if (n > 1) cost += 2 + rows_mb * static_cast<double>(n) * 0.1;
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.splits = static_cast<int>(n);
+        p.unit_tiles = unit;
+        p.places = places;
+      }
+      if (units * n > 8 * sms) break;
     }
-    if (units * n > 8 * sms) break;
   }
   // A tile without rows waits for as long as the other's whole slice: no slice may last as
   // long as a bounded wait (a tile of keys takes about 2 us, the wait a second at most).
@@ -1020,6 +1034,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
                                     bool* described) {
   a.group = a.heads / a.kv_heads;
   a.splits = plan.splits;
+  a.unit_tiles = plan.unit_tiles;
   a.places = static_cast<int>(plan.places);
   a.fault_word = fault_word_ptr();
   a.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.dv % 16 == 0 && (a.q_tokens == 1 || a.out_token % 16 == 0) &&
@@ -1045,9 +1060,11 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
   // filled, and more than one tile of keys (32 single tokens over up to 8,192 keys x 64 / 8
   // heads 114.8 us, 123.9 without; where no unit is paired they cost 3 %)
   const int64_t rows = static_cast<int64_t>(a.q_tokens) * a.group, keys = a.kv_tokens;
-  const Mode mode = rows >= 2LL * kTile * a.batch && keys >= 40LL * kTile * a.batch ? kTurns
-                    : rows <= 1LL * kTile * a.batch && keys > 1LL * kTile * a.batch * a.splits ? kPairs
-                                                                                              : kPlain;
+  const Mode mode = a.unit_tiles == 2 && rows >= 2LL * kTile * a.batch && keys >= 40LL * kTile * a.batch ? kTurns
+                    : a.unit_tiles == 1 ||
+                            (rows <= 1LL * kTile * a.batch && keys > 1LL * kTile * a.batch * a.splits)
+                        ? kPairs
+                        : kPlain;
   cudaError_t e;
   if (a.dk <= 64 && a.dv <= 64)
     e = launch<1, 1>(a, q, k, v, grid, mode, stream);
