@@ -151,7 +151,13 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) add_norm_quant_kernel(co
       }
     }
     ss = team_sum(ss);
-    float rstd = rsqrtf(ss * a.inv_dim + a.eps);
+    // The quotients do not depend on the row's factor: the values are scaled by its power of
+    // two alone, which rounds nothing, and the rest of it meets the stored scales.
+    float rstd = rsqrtf(ss * a.inv_dim + a.eps), rest = 1.f;
+    if (ss < INFINITY) {
+      rest = __int_as_float((__float_as_int(rstd) & 0x007FFFFF) | 0x3F800000);
+      rstd = __int_as_float(__float_as_int(rstd) & 0x7F800000);
+    }
     if (ss == INFINITY) {
       // squares past float's range: with values 2^-80 as large they add up to less
       // than 2^110 (a row that holds an infinity stays as it is)
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) add_norm_quant_kernel(co
       const uint32_t lo = f32x2_to_e4m3x2(q[1], q[0]) | (f32x2_to_e4m3x2(q[3], q[2]) << 16);
       const uint32_t hi = f32x2_to_e4m3x2(q[5], q[4]) | (f32x2_to_e4m3x2(q[7], q[6]) << 16);
       reinterpret_cast<uint2*>(a.codes + row * a.dim)[i] = make_uint2(lo, hi);
-      if (a.group == 0 ? i == 0 : (i & 15) == 0) a.scales[row * a.scale_groups + (a.group == 0 ? 0 : i >> 4)] = s;
+      if (a.group == 0 ? i == 0 : (i & 15) == 0) a.scales[row * a.scale_groups + (a.group == 0 ? 0 : i >> 4)] = s * rest;
     }
   }
 }
