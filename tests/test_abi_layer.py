@@ -12,7 +12,7 @@ from test_abi_operators import BIG, FAKE, INVALID, ODD, TOO_SMALL, UNSUPPORTED, 
 NAN, INF = float("nan"), float("inf")
 MORE = C.c_void_p(0x20000)
 
-ATTENTION = dict(q=FAKE, qt=16 * 192, qh=192, k=FAKE, kt=16 * 320, kh=320, v=FAKE, vt=16 * 320, vh=320, qs=FAKE, ks=FAKE,
+ATTENTION = dict(q=FAKE, qt=20 * 192, qh=192, k=FAKE, kt=16 * 320, kh=320, v=FAKE, vt=16 * 320, vh=320, qs=FAKE, ks=FAKE,
                  batch=2, nq=100, nk=100, heads=16, kv_heads=16, dk=192, dv=128, causal=1, scale=0.07, out=MORE,
                  ot=16 * 128, oh=128, lse=None, ws=None, ws_bytes=0)
 
