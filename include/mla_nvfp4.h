@@ -577,8 +577,10 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
  * sees nothing gives 0 and -inf.  Prompts, their later chunks behind earlier
  * keys, drafts and single tokens are the same call.  Scores, softmax statistics
  * and sums are float32; a weight enters the product as bf16 (off by at most
- * 2^-8 of itself).  What a token does not see never reaches its output, be it
- * infinite or NaN.
+ * 2^-8 of itself).  The largest score that a token sees, times softmax_scale and
+ * log2 e, must be less than 2^30 in magnitude: from there on, -infinity
+ * included, the token's out and lse are NaN.  What a token does not see never
+ * reaches its output, be it infinite or NaN.
  *
  *   q             device bf16 [q_tokens, num_heads, qk_dim]
  *   k, v          device bf16 [kv_tokens, num_kv_heads, qk_dim / v_dim]; not

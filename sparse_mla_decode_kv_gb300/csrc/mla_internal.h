@@ -209,8 +209,8 @@ struct PromptArgs {
   // set by the launch from the plan
   int group, splits, places, unit_tiles;
   bool out_wide;  // rows of out begin and end at multiples of 32 bytes
-  float* part_o;
-  float* part_lse;
+  float* part_o;     // [q_tokens, heads, splits, dv]
+  float2* part_lse;  // [q_tokens, heads, splits]: reference, log2 of the sum relative to it
   unsigned int* fault_word;
 };
 PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch, int heads, int kv_heads, int dv);

@@ -70,6 +70,13 @@ constexpr uint32_t kSCol = 0, kOCol = 256, kTmemCols = 512;
 constexpr int kTurnPolls = 40;  // of about 30 cycles
 constexpr int64_t kMaxSlice = 65536;  // tiles of keys
 constexpr float kLag = 8.f;
+// Scaled scores (base 2) from this magnitude on: the rounding that one FMA leaves of a row's largest
+// would be an exponent of up to 2^6 and more, and from 2^33 on its weight 0 or infinity.  A row
+// with such a score above is NaN, and one that has only such below; beside others those
+// have the weight 0 that they should.  (Exact differences for these rows cost the others 5 to
+// 25 %: whatever else happens to the scores in registers changes the order of the exponentials.)
+constexpr float kFar = 1073741824.f;  // 2^30
+constexpr float kLowest = -3.402823466e38f;  // a slice of a row that has only scores below -kFar
 constexpr float kLn2 = 0.6931471805599453f;
 // Tiles of keys that some of a CTA's rows see and others do not: what its up to 256
 // tokens see ends within 255 keys of one another, in at most three tiles.
@@ -682,9 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool raise = top - ref > kLag;
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float alpha = 1.f;
-          if (raise) {
+          if (raise && top > -kFar) {
             alpha = ex2(ref - top);  // 0 while nothing has been seen
             ref = top;
+            if (!(top < kFar)) alpha = NAN;  // stays in the sum
           }
           const uint64_t a2 = pack2(alpha, alpha);
           l2[0] = fma2(l2[0], a2, 0);
@@ -773,16 +781,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && tok0 < u.nq && !(paired && s == 1)) {
         tcgen05_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool lost = l == 0.f && lim > begin * kTile;  // keys are seen, and none has a weight
+        const float inv = lost ? NAN : l == 0.f ? 0.f : 1.f / l;
         const int64_t t = u.q0 + tok;
         const bool direct = args.splits == 1;
-        const float lse2 = l == 0.f ? -INFINITY : ref + lg2(l);
         const int64_t part = (t * args.heads + head) * args.splits + u.split;
         if (here) {
           if (!direct)
-            args.part_lse[part] = lse2;
+            args.part_lse[part] = lost ? make_float2(kLowest, kLowest) : make_float2(ref, l == 0.f ? -INFINITY : lg2(l));
           else if (args.lse != nullptr)
-            args.lse[t * args.heads + head] = lse2 * kLn2;
+            args.lse[t * args.heads + head] = lost ? NAN : l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
         }
         const bool bad = *reinterpret_cast<volatile int*>(&sm.any_bad[n % kUnits]) != 0;
 #pragma unroll 1
@@ -873,11 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins a (token, head)'s partials, a warp each, four values a lane: LSE = log2
-// sum 2^lse_s, out = sum 2^(lse_s - LSE) O_s, in one order.  A partial whose LSE
-// is -inf was not written and has no part in it.  Coherent loads: this grid may be
-// resident before the partials are written.  What bounds it is three round trips to L2,
-// made one (a token x 32 heads over 8,192 keys in 16 slices 23.2 us before, now 17.2).
+// Joins a (token, head)'s partials, a warp each, four values a lane: with slice s's
+// reference r_s and l_s = log2 of its sum, weights 2^(r_s - R + l_s - L) of the largest R
+// and L (apart, as their sum in a float would round a slice's weight by 2^-24 of R), out =
+// sum of weight O_s / sum of weights, in one order.  A partial whose l_s is -inf was not
+// written and has no part in it, nor one of kLowest unless there are no others: the row is
+// NaN.  Coherent loads: this grid may be resident before the partials are written.  What
+// bounds it is three round trips to L2, made one (a token x 32 heads over 8,192 keys in 16
+// slices 23.2 us before, now 17.2).
 constexpr int kMergeWarps = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -891,9 +902,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const Pr
   constexpr int kFirst = 8;
   const bool in = t < a.q_tokens, mine = 4 * lane < a.dv;
   const int first = __ldcg(a.q_start), last = __ldcg(a.q_start + a.batch);
-  const float* const lse = a.part_lse + at * a.splits;
+  const float2* const lse = a.part_lse + at * a.splits;
   const float* const part = a.part_o + at * a.splits * a.dv + 4 * lane;
-  const float x0 = in && lane < a.splits ? __ldcg(lse + lane) : -INFINITY;
+  const float2 none = make_float2(-INFINITY, -INFINITY);
+  const float2 x0 = in && lane < a.splits ? __ldcg(lse + lane) : none;
   float4 o[kFirst];
 #pragma unroll
   for (int s = 0; s < kFirst; ++s) {
@@ -902,15 +914,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const Pr
   }
   // tokens before the first sequence and behind the last are left as they are
   if (t < max(first, 0) || t >= min(last, a.q_tokens)) return;
-  float mx = x0;  // NaN above all
+  float mx = x0.x, ml = x0.y;  // NaN above all
   for (int s = 32 + lane; s < a.splits; s += 32) {
-    const float x = __ldcg(lse + s);
-    mx = x > mx || isnan(x) ? x : mx;
+    const float2 x = __ldcg(lse + s);
+    mx = fmaxf(mx, x.x);
+    ml = x.y > ml || isnan(x.y) ? x.y : ml;
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
-    const float x = __shfl_xor_sync(0xFFFFFFFFu, mx, d);
-    mx = x > mx || isnan(x) ? x : mx;
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    const float x = __shfl_xor_sync(0xFFFFFFFFu, ml, d);
+    ml = x > ml || isnan(x) ? x : ml;
   }
   float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
   auto add = [&](float w, float4 v) {
@@ -921,13 +935,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const Pr
     acc[2] += w * v.z;
     acc[3] += w * v.w;
   };
-  if (mx != -INFINITY) {
-    const float w0 = x0 == -INFINITY ? 0.f : ex2(x0 - mx);
+  if (mx == kLowest) {
+    sum = NAN;
+  } else if (ml != -INFINITY) {
+    auto weight = [&](float2 x) { return x.y == -INFINITY ? 0.f : ex2((x.x - mx) + (x.y - ml)); };
+    const float w0 = weight(x0);
 #pragma unroll
     for (int s = 0; s < kFirst; ++s) add(s < a.splits ? __shfl_sync(0xFFFFFFFFu, w0, s) : 0.f, o[s]);
     for (int s0 = 0; s0 < a.splits; s0 += 32) {
-      const float x = s0 == 0 ? x0 : s0 + lane < a.splits ? __ldcg(lse + s0 + lane) : -INFINITY;
-      const float w = x == -INFINITY ? 0.f : ex2(x - mx);
+      const float w = s0 == 0 ? w0 : weight(s0 + lane < a.splits ? __ldcg(lse + s0 + lane) : none);
       const int n = min(32, a.splits - s0);
 #pragma unroll 8
       for (int s = s0 == 0 ? kFirst : 0; s < n; ++s) {
@@ -942,7 +958,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const Pr
   if (4 * lane < a.dv)
     *reinterpret_cast<uint2*>(a.out + t * a.out_token + head * a.out_head + 4 * lane) =
         make_uint2(bf16x2_rn(acc[0] * inv, acc[1] * inv), bf16x2_rn(acc[2] * inv, acc[3] * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
+  if (a.lse != nullptr && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + (ml + lg2(sum))) * kLn2;
 }
 
 cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, size_t smem, void** params,
@@ -992,7 +1008,7 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
   const int64_t sms = device_sm_count();
   const int64_t tiles = (kv_tokens / batch + kTile - 1) / kTile;
   const int64_t share = (q_tokens + batch - 1) / batch;  // tokens of a sequence
-  const double rows_mb = static_cast<double>(q_tokens) * heads * (dv + 1) * 8e-6;  // of one slice, written and read
+  const double rows_mb = static_cast<double>(q_tokens) * heads * (dv + 2) * 8e-6;  // of one slice, written and read
   double best = -1;
   p.splits = 1;
   for (int unit = 2; unit >= 1; --unit) {  // tiles of rows
@@ -1026,7 +1042,7 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
   const int64_t least = ((kv_tokens + kTile - 1) / kTile + kMaxSlice - 1) / kMaxSlice;
   if (p.splits < least) p.splits = static_cast<int>(least);
   if (p.splits > 1)
-    p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 1) * sizeof(float) + 255) / 256 * 256;
+    p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 2) * sizeof(float) + 255) / 256 * 256;
   return p;
 }
 
@@ -1043,7 +1059,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
   if (a.fault_word == nullptr) return cudaErrorInvalidDevicePointer;
   if (a.splits > 1) {
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = a.part_o + static_cast<size_t>(a.q_tokens) * a.heads * a.splits * a.dv;
+    a.part_lse = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.q_tokens) * a.heads * a.splits * a.dv);
   }
   const uint32_t per = static_cast<uint32_t>(kTile / a.group);
   CUtensorMap q, k, v;
