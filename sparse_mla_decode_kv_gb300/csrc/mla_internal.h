@@ -210,7 +210,7 @@ struct PromptArgs {
   int group, splits, places, unit_tiles;
   bool out_wide;  // rows of out begin and end at multiples of 32 bytes
   float* part_o;     // [q_tokens, heads, splits, dv]
-  float2* part_lse;  // [q_tokens, heads, splits]: reference, log2 of the sum relative to it
+  float2* part_lse;  // [q_tokens, heads, splits]: reference, log2 of the sum x 2^8 relative to it
   unsigned int* fault_word;
 };
 PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch, int heads, int kv_heads, int dv);

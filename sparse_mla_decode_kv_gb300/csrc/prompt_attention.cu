@@ -3,8 +3,10 @@
 //
 // Mathematics.  Per query head and tile of 128 rows, over tiles of 128 keys:
 //   S = Q . K^T,   P = 2^(S scale - r),   O = O + P . V,   l = l + sum P
-// with r the row's running maximum, which may lag by 2^8 (P is bf16, whose range
-// is float's: a lag costs no precision), and out = O / l, lse = ln 2 (r + log2 l).
+// with r 8 above the row's maximum when it was set, and raised when a score passes it: a
+// weight is 1 at most, so O leaves float's range no earlier than a sum of weighted
+// values does (P is bf16, whose range is float's: the 2^8 cost no precision), and out =
+// O / l, lse = ln 2 (r + log2 l).
 // S, O, r and l are float; P is rounded to bf16 as V's partner in the product: a
 // key's weight in out is off by at most 2^-8 of itself, in l it is not rounded.
 //
@@ -69,7 +71,7 @@ constexpr int kCtlBytes = 2048;
 constexpr uint32_t kSCol = 0, kOCol = 256, kTmemCols = 512;
 constexpr int kTurnPolls = 40;  // of about 30 cycles
 constexpr int64_t kMaxSlice = 65536;  // tiles of keys
-constexpr float kLag = 8.f;
+constexpr float kLag = 8.f, kLagWeight = 256.f;  // 2^8
 // Scaled scores (base 2) from this magnitude on: the rounding that one FMA leaves of a row's largest
 // would be an exponent of up to 2^6 and more, and from 2^33 on its weight 0 or infinity.  A row
 // with such a score above is NaN, and one that has only such below; beside others those
@@ -686,12 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float top = fmaxf(most[0], most[1]) * sl;
-        const bool raise = top - ref > kLag;
+        const bool raise = top > ref;
         if (__any_sync(0xFFFFFFFFu, raise)) {
           float alpha = 1.f;
           if (raise && top > -kFar) {
-            alpha = ex2(ref - top);  // 0 while nothing has been seen
-            ref = top;
+            alpha = ex2(ref - (top + kLag));  // 0 while nothing has been seen
+            ref = top + kLag;
             if (!(top < kFar)) alpha = NAN;  // stays in the sum
           }
           const uint64_t a2 = pack2(alpha, alpha);
@@ -788,9 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part = (t * args.heads + head) * args.splits + u.split;
         if (here) {
           if (!direct)
-            args.part_lse[part] = lost ? make_float2(kLowest, kLowest) : make_float2(ref, l == 0.f ? -INFINITY : lg2(l));
+            args.part_lse[part] = lost ? make_float2(kLowest, kLowest) : make_float2(ref, l == 0.f ? -INFINITY : lg2(l * kLagWeight));
           else if (args.lse != nullptr)
-            args.lse[t * args.heads + head] = lost ? NAN : l == 0.f ? -INFINITY : (ref + lg2(l)) * kLn2;
+            args.lse[t * args.heads + head] = lost ? NAN : l == 0.f ? -INFINITY : (ref - kLag + lg2(l * kLagWeight)) * kLn2;
         }
         const bool bad = *reinterpret_cast<volatile int*>(&sm.any_bad[n % kUnits]) != 0;
 #pragma unroll 1
@@ -882,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins a (token, head)'s partials, a warp each, four values a lane: with slice s's
-// reference r_s and l_s = log2 of its sum, weights 2^(r_s - R + l_s - L) of the largest R
+// reference r_s and l_s = log2 of its sum x 2^8, weights 2^(r_s - R + l_s - L) of the largest R
 // and L (apart, as their sum in a float would round a slice's weight by 2^-24 of R), out =
 // sum of weight O_s / sum of weights, in one order.  A partial whose l_s is -inf was not
 // written and has no part in it, nor one of kLowest unless there are no others: the row is
@@ -958,7 +960,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prompt_merge_kernel(const Pr
   if (4 * lane < a.dv)
     *reinterpret_cast<uint2*>(a.out + t * a.out_token + head * a.out_head + 4 * lane) =
         make_uint2(bf16x2_rn(acc[0] * inv, acc[1] * inv), bf16x2_rn(acc[2] * inv, acc[3] * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + (ml + lg2(sum))) * kLn2;
+  if (a.lse != nullptr && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx - kLag + (ml + lg2(sum))) * kLn2;
 }
 
 cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, size_t smem, void** params,

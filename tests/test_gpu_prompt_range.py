@@ -88,3 +88,27 @@ def test_scores_of_minus_infinity(nk):
     out, _ = m.mla_prompt_attention(q.to(torch.bfloat16), k.to(torch.bfloat16), v, starts([2]), starts([nk]), 0.5, lse=lse)
     assert out[0].isnan().all() and lse[0].isnan().all()
     assert torch.equal(out[1], v[-1]) and lse[1].abs().item() <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("nq,heads,nk", [(1, 1, 129), (1, 1, 4000), (1, 1, 30000), (128, 160, 300), (300, 90, 129),
+                                         (300, 90, 256), (300, 90, 700), (600, 40, 6000)])
+@pytest.mark.parametrize("step", [1, 7, 8, 9])
+def test_values_near_the_largest_float(nq, heads, nk, step):
+    """The last key's score is `step` (base 2) above the ones before it, its values are 2^127: weighted
+    sums with weights up to 1 stay floats.  out = 2^127 / (1 + (nk - 1) 2^-step) up to the
+    tolerances above, the weights' rounding to bf16 (2^-8) and twice what the sum is off by: the
+    scores' product with the scale and difference to the reference 4 x 2^-24 of up to 2^5, ex2
+    2^-22, the sums of nk weights (nk / 4 + 16) x 2^-24."""
+    m = lib()
+    q, k = torch.zeros((nq, heads, 64), device=DEV), torch.zeros((nk, heads, 64), device=DEV)
+    v = torch.zeros((nk, heads, 64), device=DEV)
+    q[..., 0], k[-1, :, 0], v[-1] = 1, step, 2.0 ** 127
+    v[:, :, 1] = 2.0 ** -120  # and a value that all have, near the other end
+    out, _ = m.mla_prompt_attention(q.to(torch.bfloat16), k.to(torch.bfloat16), v.to(torch.bfloat16), starts([nq]),
+                                    starts([nk]), math.log(2.0), causal=False)
+    want = 2.0 ** 127 / (1 + (nk - 1) * 2.0 ** -step)
+    tol = 2 * 2.0 ** -8 + nk / 16 * 2.0 ** -22 + 2 * (2.0 ** -17 + 2.0 ** -22 + (nk / 4 + 16) * 2.0 ** -24)
+    got = out.double()
+    rest = torch.cat([got[..., :1], got[..., 2:]], -1)
+    assert ((rest / want - 1).abs() <= tol).all(), (rest / want - 1).abs().max().item()
+    assert ((got[..., 1] * 2.0 ** 120 - 1).abs() <= tol).all(), got[..., 1].max().item() * 2.0 ** 120
