@@ -605,8 +605,9 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
  *                 256-byte aligned (that size depends on the current device
  *                 and may be 0); contents on entry do not matter; calls that
  *                 may run at the same time need one each
- * batch == 0 or q_tokens == 0 is a no-op.  At most 2^31 - 256 tokens, and
- * q_tokens x num_heads < 2^31 (more: MLA_ERR_UNSUPPORTED).
+ * batch == 0 or q_tokens == 0 is a no-op.  At most 2^31 - 256 tokens and
+ * sequences, and q_tokens x num_heads and batch x num_kv_heads < 2^31 (more:
+ * MLA_ERR_UNSUPPORTED).
  */
 size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
                                            int num_kv_heads, int v_dim);

@@ -179,6 +179,13 @@ mla_status_t check_norm_rope(const mla_heads_t* q, const mla_heads_t* k, int64_t
 constexpr int kMaxNormDim = 16384;
 constexpr int64_t kMaxTokens = 0x7FFFFF00;  // of a packed batch: a tile past the last still has a 32-bit number
 
+// Sizes of a packed batch for which every number that the plan and the kernels form fits: of
+// the search through the sequences (up to batch + 32), of rows, and of units of work.
+bool prompt_sizes_fit(int64_t q_tokens, int64_t kv_tokens, int64_t batch, int64_t num_heads, int64_t num_kv_heads) {
+  return q_tokens <= kMaxTokens && kv_tokens <= kMaxTokens && batch <= kMaxTokens &&
+         q_tokens * num_heads <= 0x7FFFFFFF && batch * num_kv_heads <= 0x7FFFFFFF;
+}
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -841,8 +848,9 @@ mla_status_t mla_fp4_matvec(const void* x, mla_x_type_t x_type, int64_t x_token_
 
 size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
                                            int num_kv_heads, int v_dim) {
-  if (q_tokens <= 0 || q_tokens > kMaxTokens || kv_tokens < 0 || kv_tokens > kMaxTokens || batch <= 0 ||
-      num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 128 || v_dim < 8)
+  if (q_tokens <= 0 || kv_tokens < 0 || batch <= 0 || num_kv_heads < 1 || num_heads < 1 ||
+      num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 128 || v_dim < 8 ||
+      !prompt_sizes_fit(q_tokens, kv_tokens, batch, num_heads, num_kv_heads))
     return 0;
   return plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim).workspace;
 }
@@ -862,6 +870,7 @@ mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int
   if (qk_dim > 192 || v_dim > 128 || num_heads / num_kv_heads > 128 || q_tokens > kMaxTokens || kv_tokens > kMaxTokens)
     return MLA_ERR_UNSUPPORTED;
   if (batch == 0 || q_tokens == 0) return MLA_OK;
+  if (!prompt_sizes_fit(q_tokens, kv_tokens, batch, num_heads, num_kv_heads)) return MLA_ERR_UNSUPPORTED;
   if (!q || !query_start || !kv_start || !out || (kv_tokens > 0 && (!k || !v))) return MLA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(query_start, 4) ||
       !aligned(kv_start, 4) || !aligned(lse, 4))
@@ -882,8 +891,7 @@ mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int
       rows_overlap(q_tokens, out_token_stride, num_heads, out_head_stride, v_dim))
     return MLA_ERR_INVALID_ARG;
   const PromptPlan plan = plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim);
-  if (plan.places * num_kv_heads * plan.splits > 0x7FFFFFFF || q_tokens * num_heads > 0x7FFFFFFF)
-    return MLA_ERR_UNSUPPORTED;
+  if (plan.places * num_kv_heads * plan.splits > 0x7FFFFFFF) return MLA_ERR_UNSUPPORTED;
   if (plan.workspace > 0) {
     if (workspace_bytes < plan.workspace) return MLA_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;

@@ -102,3 +102,26 @@ def test_fp4_matvec(m, over, status):  # noqa: F811
 ])
 def test_prompt_attention_strides(m, over, status):  # noqa: F811
     assert call(m, "mla_prompt_attention", ATTENTION, over) == status
+
+
+LARGE = 2 ** 31 - 256  # tokens, sequences
+
+
+@pytest.mark.parametrize("over,status", [
+    # sequences whose search would leave 32 bits
+    *[(dict(batch=2 ** 31 - n, nq=1, nk=1, heads=1, kv_heads=1), UNSUPPORTED) for n in (1, 20, 32, 255)],
+    # units of work: sequences x key heads x slices that are 0 or a few modulo 2^64
+    (dict(batch=2 ** 30, nq=1, nk=LARGE, heads=2 ** 30, kv_heads=2 ** 30, qt=2 ** 39, kt=2 ** 39, vt=2 ** 39), UNSUPPORTED),
+    (dict(batch=2 ** 30 + 1, nq=1, nk=LARGE, heads=2 ** 30, kv_heads=2 ** 30, qt=2 ** 39, kt=2 ** 39, vt=2 ** 39), UNSUPPORTED),
+    (dict(batch=2 ** 16, nq=1, nk=1, heads=2 ** 15, kv_heads=2 ** 15), UNSUPPORTED),
+    (dict(batch=LARGE + 1, nq=0), 0),
+])
+def test_prompt_attention_largest_sizes(m, over, status):  # noqa: F811
+    assert call(m, "mla_prompt_attention", ATTENTION, over) == status
+
+
+def test_prompt_attention_workspace_of_refused_sizes(m):  # noqa: F811
+    size = m.mla_prompt_attention_workspace_size
+    assert size(1, LARGE, LARGE + 1, 1, 1, 64) == 0
+    assert size(1, LARGE, 2 ** 30, 2 ** 30, 2 ** 30, 64) == 0
+    assert size(2 ** 27, LARGE, 1, 64, 64, 64) == 0
