@@ -151,25 +151,28 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256) add_norm_quant_kernel(co
       }
     }
     ss = team_sum(ss);
-    // The quotients do not depend on the row's factor: the values are scaled by its power of
-    // two alone, which rounds nothing, and the rest of it meets the stored scales.
-    float rstd = rsqrtf(ss * a.inv_dim + a.eps), rest = 1.f;
-    if (ss < INFINITY) {
-      rest = __int_as_float((__float_as_int(rstd) & 0x007FFFFF) | 0x3F800000);
-      rstd = __int_as_float(__float_as_int(rstd) & 0x7F800000);
-    }
-    if (ss == INFINITY) {
-      // squares past float's range: with values 2^-80 as large they add up to less
-      // than 2^110 (a row that holds an infinity stays as it is)
+    float mean = ss * a.inv_dim + a.eps, down = 1.f;
+    if (mean == INFINITY) {
+      // squares, or the largest eps with them, past float's range: with values 2^-80 as large
+      // they add up to less than 2^110 (a row that holds an infinity stays as it is)
+      constexpr float kDown = 8.271806125530277e-25f;  // 2^-80
       float small = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float v = h[c][k] * 8.271806125530277e-25f;  // 2^-80
+          const float v = h[c][k] * kDown;
           small = fmaf(v, v, small);
         }
-      rstd = rsqrtf(team_sum(small) * a.inv_dim) * 8.271806125530277e-25f;
+      mean = fmaf(team_sum(small), a.inv_dim, a.eps * kDown * kDown);
+      down = kDown;
+    }
+    // The quotients do not depend on the row's factor: the values are scaled by its power of
+    // two alone, which rounds nothing, and the rest of it meets the stored scales.
+    float rstd = rsqrtf(mean), rest = 1.f;
+    if (mean < INFINITY) {
+      rest = __int_as_float((__float_as_int(rstd) & 0x007FFFFF) | 0x3F800000);
+      rstd = __int_as_float(__float_as_int(rstd) & 0x7F800000) * down;
     }
     uint32_t mx[C];
 #pragma unroll
