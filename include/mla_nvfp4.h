@@ -611,6 +611,19 @@ mla_status_t mla_prefix_decode(const uint16_t* q_nope, const uint16_t* q_rope, c
  */
 size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads,
                                            int num_kv_heads, int v_dim);
+
+/*
+ * How a call of these sizes is divided on the current device.  A unit is
+ * *row_tiles (1 or 2) times 128 rows of one sequence and key head, with all of
+ * its keys or one of *slices parts of them (several are joined by a second
+ * kernel); *units is the number of CTAs in the grid: as many as the device has
+ * SMs run, and take over the others' units (some of which may be empty, as
+ * lengths are known on the device only).  *variant: 0 plain, 1 the
+ * exponentials of a unit's two tiles take turns, 2 a unit of one filled tile has its
+ * keys shared by two halves.  Output pointers may be NULL.
+ */
+mla_status_t mla_prompt_attention_plan(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads, int num_kv_heads,
+                                       int v_dim, int* row_tiles, int* slices, int64_t* units, int* variant);
 mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* k,
                                   int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
                                   int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,

@@ -26,7 +26,8 @@ __all__ = [
     "mla_sparse_decode_staged", "mla_sparse_decode_mtp_workspace_size", "mla_sparse_decode_mtp",
     "mla_block_table_extend", "mla_qk_norm_rope", "mla_kv_norm_rope_append", "mla_window_decode_workspace_size",
     "mla_window_decode", "mla_prefix_decode_workspace_size", "mla_prefix_decode",
-    "mla_prompt_attention_workspace_size", "mla_prompt_attention", "mla_add_norm_quant", "mla_fp4_matvec",
+    "mla_prompt_attention_workspace_size", "mla_prompt_attention_plan", "mla_prompt_attention", "mla_add_norm_quant",
+    "mla_fp4_matvec",
 ]
 
 MLA_KV_NVFP4 = 0
@@ -88,6 +89,7 @@ SIGNATURES = {
     "mla_prefix_decode": (_I32, [_P, _P, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F32,
                                  _I32, _P, _P, _P, _SZ, _P]),
     "mla_prompt_attention_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I32]),
+    "mla_prompt_attention_plan": (_I32, [_I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
     "mla_prompt_attention": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32,
                                     _I32, _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "mla_add_norm_quant": (_I32, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _F32, _P, _P, _P]),
@@ -706,6 +708,20 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
 def mla_prompt_attention_workspace_size(q_tokens: int, kv_tokens: int, batch: int, num_heads: int, num_kv_heads: int,
                                         v_dim: int) -> int:
     return int(load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim))
+
+
+def mla_prompt_attention_plan(q_tokens: int, kv_tokens: int, batch: int, num_heads: int, num_kv_heads: int,
+                              v_dim: int) -> dict:
+    """{"row_tiles", "slices", "units", "variant"} of a call of these sizes on the current device;
+    variant is "plain", "turns" or "pairs"."""
+    for v, name in ((batch, "batch"), (num_heads, "num_heads"), (num_kv_heads, "num_kv_heads"), (v_dim, "v_dim")):
+        _c_int(v, name)
+    tiles, slices, units, variant = C.c_int(), C.c_int(), C.c_int64(), C.c_int()
+    _check("mla_prompt_attention_plan",
+           load().mla_prompt_attention_plan(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim, C.byref(tiles),
+                                            C.byref(slices), C.byref(units), C.byref(variant)))
+    return {"row_tiles": tiles.value, "slices": slices.value, "units": units.value,
+            "variant": ("plain", "turns", "pairs")[variant.value]}
 
 
 @functools.lru_cache(maxsize=1024)

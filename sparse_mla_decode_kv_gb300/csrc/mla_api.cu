@@ -855,6 +855,22 @@ size_t mla_prompt_attention_workspace_size(int64_t q_tokens, int64_t kv_tokens, 
   return plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim).workspace;
 }
 
+mla_status_t mla_prompt_attention_plan(int64_t q_tokens, int64_t kv_tokens, int batch, int num_heads, int num_kv_heads,
+                                       int v_dim, int* row_tiles, int* slices, int64_t* units, int* variant) {
+  if (q_tokens <= 0 || kv_tokens < 0 || batch <= 0 || num_kv_heads < 1 || num_heads < 1 ||
+      num_heads % num_kv_heads != 0 || v_dim < 8 || v_dim % 8 != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (v_dim > 128 || num_heads / num_kv_heads > 128 ||
+      !prompt_sizes_fit(q_tokens, kv_tokens, batch, num_heads, num_kv_heads))
+    return MLA_ERR_UNSUPPORTED;
+  const PromptPlan plan = plan_prompt_attention(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim);
+  if (row_tiles) *row_tiles = plan.unit_tiles;
+  if (slices) *slices = plan.splits;
+  if (units) *units = plan.places * num_kv_heads * plan.splits;
+  if (variant) *variant = plan.variant;
+  return MLA_OK;
+}
+
 mla_status_t mla_prompt_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* k,
                                   int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
                                   int64_t v_token_stride, int64_t v_head_stride, const int32_t* query_start,

@@ -184,10 +184,12 @@ struct NormRopeArgs {
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 
 // Attention over packed prompts (prompt_attention.cu).
+enum PromptVariant { kPromptPlain, kPromptTurns, kPromptPairs };
 struct PromptPlan {
   int64_t places;    // of units, per key head
   int unit_tiles;    // tiles of rows in a unit: 1 or 2
   int splits;        // CTAs per pair along the keys
+  PromptVariant variant;
   size_t workspace;  // bytes of partials, 0 for a single slice
 };
 struct PromptArgs {

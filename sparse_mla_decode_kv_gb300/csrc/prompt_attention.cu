@@ -329,10 +329,9 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int id, int lane,
   return true;
 }
 
-// kTurns: the two tiles' exponentials take turns, see there.  kPairs: where a sequence's rows
+// Turns: the two tiles' exponentials take turns, see there.  Pairs: where a sequence's rows
 // fill one tile at most, the other one has the same rows and every second tile of keys.
-enum Mode { kPlain, kTurns, kPairs };
-template <int KC, int VC, Mode kMode>
+template <int KC, int VC, PromptVariant kVariant>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const PromptArgs args, const __grid_constant__ CUtensorMap q_map,
                             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -407,14 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (uint32_t asked = 0; ok && id >= 0; ++asked) {
         Unit u;
-        if (find_unit(args, id, lane, kMode == kPairs, u)) {
+        if (find_unit(args, id, lane, kVariant == kPromptPairs, u)) {
           if (n >= kUnits) ok = wait_bar_warp(sm, &sm.unit_free[n % kUnits], unit_parity(n - kUnits), fw);
           if (ok && leader) {
             sm.unit[n % kUnits] = u;
             sm.any_bad[n % kUnits] = 0;
             for (int i = 0; i < kMaskedTiles * (kTile / 32); ++i) sm.bad[n % kUnits][0][i] = 0;
             mbar_arrive(&sm.unit_full[n % kUnits]);
-            const int items = 2 * (kMode == kPairs ? u.steps : max(u.count[0], u.count[1]));
+            const int items = 2 * (kVariant == kPromptPairs ? u.steps : max(u.count[0], u.count[1]));
             auto copy_q = [&](int s) {
               if (q_uses[s] > 0) ok = wait_bar(sm, &sm.q_free[s], (q_uses[s] - 1) & 1u, fw);
               if (!ok) return;
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++q_uses[s];
               for (int c = 0; c < KC; ++c)
                 tma_load_3d(s_q + (s * KC + c) * kChunkBytes, &q_map, 64 * c, u.head * args.group,
-                            u.q0 + u.tok + (kMode == kPairs && u.paired ? 0 : s * per), &sm.q_full[s]);
+                            u.q0 + u.tok + (kVariant == kPromptPairs && u.paired ? 0 : s * per), &sm.q_full[s]);
             };
             for (int i = 0; i < items && ok; ++i) {
               const int chunks = (i & 1) ? VC : KC;
@@ -498,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_bar(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
           if (!ok || sm.unit[n % kUnits].last) break;
           const int count = s == 0 ? sm.unit[n % kUnits].count[0] : sm.unit[n % kUnits].count[1];
-          const int n_tiles = kMode == kPairs ? sm.unit[n % kUnits].steps
+          const int n_tiles = kVariant == kPromptPairs ? sm.unit[n % kUnits].steps
                                               : max(count, s == 0 ? sm.unit[n % kUnits].count[1] : sm.unit[n % kUnits].count[0]);
           // of a paired unit's tiles of keys every other one is this tile's
-          const bool paired = kMode == kPairs && sm.unit[n % kUnits].paired;
+          const bool paired = kVariant == kPromptPairs && sm.unit[n % kUnits].paired;
           auto ours = [&](int j) { return paired ? (j & 1) == s : j < count; };
           auto nth = [&](int j) { return paired ? j >> 1 : j; };
           mbar_arrive(&sm.unit_free[n % kUnits]);
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar_warp(sm, &sm.unit_full[n % kUnits], unit_parity(n), fw);
         if (!ok || sm.unit[n % kUnits].last) break;
         const Unit& u = sm.unit[n % kUnits];
-        const int n_tiles = kMode == kPairs ? u.steps : max(u.count[0], u.count[1]);
+        const int n_tiles = kVariant == kPromptPairs ? u.steps : max(u.count[0], u.count[1]);
         const int masked0 = u.first_masked - u.begin;  // tiles from this one on
         const int seen = visible(args, u.nq, u.nk, u.tok);  // keys before it are seen by all rows
         for (int j = 0; j < n_tiles && ok; ++j) {
@@ -656,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || sm.unit[n % kUnits].last) break;
       const Unit& u = sm.unit[n % kUnits];
       const int count = s == 0 ? u.count[0] : u.count[1];
-      const bool paired = kMode == kPairs && u.paired;
+      const bool paired = kVariant == kPromptPairs && u.paired;
       const int tok0 = u.tok + (paired ? 0 : s * per), tok = tok0 + row_tok;
       const int head = u.head * args.group + row_head;
       const bool here = row < rows && tok < u.nq;
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // waited long enough goes on.  It pays over many tiles of keys (x 16 heads, with
         // and without): 16,384 tokens of 192 dims 805 and 868 us, of 128 693 and 767, 6,000
         // of 192 134 and 142; 2 x 4,096 of 128 124 and 118, 2 x 3,000 of 192 91 and 85.
-        if (kMode == kTurns) {
+        if (kVariant == kPromptTurns) {
           for (int i = 0; i < kTurnPolls && *reinterpret_cast<volatile int*>(&sm.busy[s ^ 1][quad]) != 0; ++i) {
           }
           if (lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 1;
@@ -745,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part == 2) publish(0);
           tmem_st16(s_addr + 16 * part, p);
         }
-        if (kMode == kTurns && lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 0;
+        if (kVariant == kPromptTurns && lane == 0) *reinterpret_cast<volatile int*>(&sm.busy[s][quad]) = 0;
         publish(1);
       }
       // ---- output
@@ -981,12 +980,13 @@ cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, 
 
 template <int KC, int VC>
 cudaError_t launch(PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, unsigned grid,
-                   Mode mode, cudaStream_t stream) {
-  const void* kernel = mode == kTurns   ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kTurns>)
-                       : mode == kPairs ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPairs>)
-                                        : reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPlain>);
+                   PromptVariant variant, cudaStream_t stream) {
+  const void* kernel = variant == kPromptTurns ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPromptTurns>)
+                       : variant == kPromptPairs
+                           ? reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPromptPairs>)
+                           : reinterpret_cast<const void*>(prompt_attention_kernel<KC, VC, kPromptPlain>);
   static std::atomic<uint64_t> configured[3];
-  const cudaError_t e = set_smem_limit_once(kernel, kSmemBytes, &configured[mode]);
+  const cudaError_t e = set_smem_limit_once(kernel, kSmemBytes, &configured[variant]);
   if (e != cudaSuccess) return e;
   void* params[] = {&a, const_cast<CUtensorMap*>(&q), const_cast<CUtensorMap*>(&k), const_cast<CUtensorMap*>(&v)};
   return launch_dependent(kernel, grid, kThreads, kSmemBytes, params, stream);
@@ -1043,6 +1043,14 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
   // long as a bounded wait (a tile of keys takes about 2 us, the wait a second at most).
   const int64_t least = ((kv_tokens + kTile - 1) / kTile + kMaxSlice - 1) / kMaxSlice;
   if (p.splits < least) p.splits = static_cast<int>(least);
+  // turns: both tiles filled, and 40 tiles of keys or more, on average; pairs: at most one tile
+  // filled, and more than one tile of keys (32 single tokens over up to 8,192 keys x 64 / 8
+  // heads 114.8 us, 123.9 without; where no unit is paired they cost 3 %)
+  const int64_t rows = q_tokens * group;
+  p.variant = p.unit_tiles == 2 && rows >= 2LL * kTile * batch && kv_tokens >= 40LL * kTile * batch ? kPromptTurns
+              : p.unit_tiles == 1 || (rows <= 1LL * kTile * batch && kv_tokens > 1LL * kTile * batch * p.splits)
+                  ? kPromptPairs
+                  : kPromptPlain;
   if (p.splits > 1)
     p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 2) * sizeof(float) + 255) / 256 * 256;
   return p;
@@ -1074,22 +1082,13 @@ cudaError_t launch_prompt_attention(PromptArgs a, const PromptPlan& plan, void* 
                encode_tensor_map_3d(&v, have ? a.v : a.q, a.dv, kv_heads, kv_rows, 2 * a.v_head, 2 * a.v_token, 1, kTile);
   if (!*described) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(plan.places * a.kv_heads * a.splits);
-  // turns: both tiles filled, and 40 tiles of keys or more, on average; pairs: at most one tile
-  // filled, and more than one tile of keys (32 single tokens over up to 8,192 keys x 64 / 8
-  // heads 114.8 us, 123.9 without; where no unit is paired they cost 3 %)
-  const int64_t rows = static_cast<int64_t>(a.q_tokens) * a.group, keys = a.kv_tokens;
-  const Mode mode = a.unit_tiles == 2 && rows >= 2LL * kTile * a.batch && keys >= 40LL * kTile * a.batch ? kTurns
-                    : a.unit_tiles == 1 ||
-                            (rows <= 1LL * kTile * a.batch && keys > 1LL * kTile * a.batch * a.splits)
-                        ? kPairs
-                        : kPlain;
   cudaError_t e;
   if (a.dk <= 64 && a.dv <= 64)
-    e = launch<1, 1>(a, q, k, v, grid, mode, stream);
+    e = launch<1, 1>(a, q, k, v, grid, plan.variant, stream);
   else if (a.dk <= 128)
-    e = launch<2, 2>(a, q, k, v, grid, mode, stream);
+    e = launch<2, 2>(a, q, k, v, grid, plan.variant, stream);
   else
-    e = launch<3, 2>(a, q, k, v, grid, mode, stream);
+    e = launch<3, 2>(a, q, k, v, grid, plan.variant, stream);
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t pairs = static_cast<int64_t>(a.q_tokens) * a.heads;
   void* merge[] = {&a};
