@@ -1043,14 +1043,16 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
   // long as a bounded wait (a tile of keys takes about 2 us, the wait a second at most).
   const int64_t least = ((kv_tokens + kTile - 1) / kTile + kMaxSlice - 1) / kMaxSlice;
   if (p.splits < least) p.splits = static_cast<int>(least);
-  // turns: both tiles filled, and 40 tiles of keys or more, on average; pairs: at most one tile
+  // turns: both tiles filled, and 40 tiles of keys a slice or more, on average (without and with:
+  // 700 tokens x 16 heads of 192 over 5,200 keys in 3 slices 48 and 52 us, 2,600 x 20 of 64 over
+  // 5,400 in 2 105 and 112); pairs: at most one tile
   // filled, and more than one tile of keys (32 single tokens over up to 8,192 keys x 64 / 8
   // heads 114.8 us, 123.9 without; where no unit is paired they cost 3 %)
   const int64_t rows = q_tokens * group;
-  p.variant = p.unit_tiles == 2 && rows >= 2LL * kTile * batch && kv_tokens >= 40LL * kTile * batch ? kPromptTurns
-              : p.unit_tiles == 1 || (rows <= 1LL * kTile * batch && kv_tokens > 1LL * kTile * batch * p.splits)
-                  ? kPromptPairs
-                  : kPromptPlain;
+  const int64_t slice_keys = 1LL * kTile * batch * p.splits;  // a tile of keys for every slice
+  p.variant = p.unit_tiles == 2 && rows >= 2LL * kTile * batch && kv_tokens >= 40 * slice_keys ? kPromptTurns
+              : p.unit_tiles == 1 || (rows <= 1LL * kTile * batch && kv_tokens > slice_keys)   ? kPromptPairs
+                                                                                             : kPromptPlain;
   if (p.splits > 1)
     p.workspace = (static_cast<size_t>(q_tokens) * heads * p.splits * (dv + 2) * sizeof(float) + 255) / 256 * 256;
   return p;

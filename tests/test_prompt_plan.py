@@ -34,6 +34,8 @@ def test_plan_and_workspace(m, sizes):
 def test_variants(m):
     plan = m.mla_prompt_attention_plan
     assert plan(4096, 5200, 1, 16, 16, 128)["variant"] == "turns"     # both tiles, many keys
+    sliced = plan(700, 5200, 1, 16, 16, 128)                          # as many keys, but few a slice
+    assert sliced["slices"] > 1 and sliced["variant"] == "plain"
     assert plan(9600, 9600, 24, 16, 16, 128)["variant"] == "plain"    # both tiles, few keys
     assert plan(32, 150000, 32, 64, 8, 128)["variant"] == "pairs"     # a token each
     assert plan(600, 18000, 3, 4, 2, 128)["row_tiles"] == 1           # rows that leave SMs idle
