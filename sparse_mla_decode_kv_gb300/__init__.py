@@ -707,6 +707,7 @@ def mla_prefix_decode(q_nope, q_rope, kv_pool, kv_block_stride, num_blocks, pref
 # --------------------------------------------------------------------- prompts, and around the attention of a layer
 def mla_prompt_attention_workspace_size(q_tokens: int, kv_tokens: int, batch: int, num_heads: int, num_kv_heads: int,
                                         v_dim: int) -> int:
+    _c_ints(batch=batch, num_heads=num_heads, num_kv_heads=num_kv_heads, v_dim=v_dim)
     return int(load().mla_prompt_attention_workspace_size(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim))
 
 
@@ -714,8 +715,7 @@ def mla_prompt_attention_plan(q_tokens: int, kv_tokens: int, batch: int, num_hea
                               v_dim: int) -> dict:
     """{"row_tiles", "slices", "units", "variant"} of a call of these sizes on the current device;
     variant is "plain", "turns" or "pairs"."""
-    for v, name in ((batch, "batch"), (num_heads, "num_heads"), (num_kv_heads, "num_kv_heads"), (v_dim, "v_dim")):
-        _c_int(v, name)
+    _c_ints(batch=batch, num_heads=num_heads, num_kv_heads=num_kv_heads, v_dim=v_dim)
     tiles, slices, units, variant = C.c_int(), C.c_int(), C.c_int64(), C.c_int()
     _check("mla_prompt_attention_plan",
            load().mla_prompt_attention_plan(q_tokens, kv_tokens, batch, num_heads, num_kv_heads, v_dim, C.byref(tiles),

@@ -59,3 +59,12 @@ def test_heads_and_sequences(m):
         q, at = Wide((1, heads, dk), BF16), Wide((batch + 1,), I32)
         with pytest.raises(ValueError, match="32 bits"):
             m.mla_prompt_attention(q, q, q, at, at, 1.0)
+
+
+@pytest.mark.parametrize("query", ["mla_prompt_attention_workspace_size", "mla_prompt_attention_plan"])
+def test_sizes_of_a_prompt_batch(m, query):
+    for at in (2, 3, 4, 5):
+        sizes = [32, 10 ** 6, 32, 8, 1, 128]
+        sizes[at] += 2 ** 32
+        with pytest.raises(ValueError, match="32 bits"):
+            getattr(m, query)(*sizes)
