@@ -789,7 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part = (t * args.heads + head) * args.splits + u.split;
         if (here) {
           if (!direct)
-            args.part_lse[part] = lost ? make_float2(kLowest, kLowest) : make_float2(ref, l == 0.f ? -INFINITY : lg2(l * kLagWeight));
+            args.part_lse[part] = lost       ? make_float2(kLowest, kLowest)
+                                  : l == 0.f ? make_float2(-INFINITY, -INFINITY)
+                                             : make_float2(ref, lg2(l * kLagWeight));
           else if (args.lse != nullptr)
             args.lse[t * args.heads + head] = lost ? NAN : l == 0.f ? -INFINITY : (ref - kLag + lg2(l * kLagWeight)) * kLn2;
         }
