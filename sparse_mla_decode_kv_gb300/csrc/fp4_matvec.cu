@@ -22,14 +22,19 @@
 // Sums of warps and CTAs are joined in one order: a call gives the same bits
 // every time.
 //
-// Bound: HBM, 9/16 byte a weight, and for these matrices the unpacking before it.
-// 16 rows x 128 values take a warp 107 instructions with up to 8 tokens, 64 cycles of
-// an SM: 4.6 to 4.8 TB/s where memory gives 6.8 (without the scales' multiplications
-// 5.8), plus 4 us of start and end.  One token x 12288 x 6144 14.4 us, 2,950 GB/s; x
-// 128,000 x 6144 94 us, 4,700; four x 24583 x 6144 25.4 us, 3,360.  With 32 tokens it is
-// 290 instructions and 150 cycles (the tokens' conversion, the products): x 6144 x 12288
-// 28.8 us.  Weights that were started on their way to L2 as a whole before the tokens
-// were laid out gained nothing any more: 14.5, 107, 27.0, 27.5 us.
+// Bound: HBM, 9/16 byte a weight, and for these matrices latency and the unpacking.
+// Memory latency is the first stall (four tokens: long_scoreboard 4.5 warps an issue, 51 %
+// of the issue slots used, 35 % of the warps resident).  16 rows x 128 values take a warp
+// 107 instructions with up to 8 tokens, 64 cycles of an SM: 4.6 to 4.8 TB/s where memory
+// gives 6.8 (without the scales' multiplications 5.8), plus 4 us of start and end.  One
+// token x 12288 x 6144 14.4 us, 2,950 GB/s; x 128,000 x 6144 97 us, 4,560; four x 24583 x
+// 6144 25.2 us, 3,390.  With 32 tokens it is 290 instructions and 150 cycles (the tokens'
+// conversion, the products): x 6144 x 12288 28.7 us.
+//
+// The weights' way to L2 is not started as a whole while the tokens are laid out.  That
+// takes 5 % off 9 to 32 e4m3 tokens (32 x 6144 x 12288 28.1 to 26.6 us, x 12288 x 6144 28.7
+// to 27.2), but adds 10 to 13 % to as many bf16 ones, whose layout takes longer (x 6144 x
+// 6144 19.4 to 21.3, x 8192 x 16384 44.4 to 49.2), 6 % to four and 18 % to the 128,000 rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

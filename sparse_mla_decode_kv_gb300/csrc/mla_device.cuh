@@ -28,11 +28,12 @@ constexpr int kIdxDim = 128;               // indexer key width (e4m3)
 constexpr unsigned int kFaultDecodeWait = 1u;
 constexpr unsigned int kFaultIndexerWait = 2u;
 constexpr unsigned int kFaultPromptWait = 4u;
-// Poll budget of the back-off phase of a bounded wait (each poll sleeps a
-// few microseconds): about a second in total, with the hinted phase before
-// it, far beyond any legitimate wait in these kernels (microseconds).  Polls
-// do not advance while the context is switched out, so time-slicing with
-// other work does not make a wait give up early.
+// Poll budget of the back-off phase of a bounded wait: with the hinted phase
+// before it 1.1 s on a barrier that nothing completes.  Hints are upper bounds and
+// sleeps approximate, so less may pass; legitimate waits are microseconds, but for
+// the prompt attention's, where a role without rows waits for a slice of at most
+// 65,536 tiles of keys (0.15 s).  Polls do not advance while the context is
+// switched out, so time-slicing with other work does not make a wait give up early.
 constexpr uint32_t kWaitPolls = 1u << 18;
 
 // ---- conversions -----------------------------------------------------------

@@ -13,8 +13,9 @@
 // Rows.  The G query heads of a key head share its keys: a tile is 128 / G tokens
 // x G heads, so a few tokens of many heads fill it as well as many tokens of one.
 //
-// Work split.  A unit is two tiles of one sequence and key head and (a slice of)
-// their keys; the tensor core works on one tile while the other's softmax runs.
+// Work split.  A unit is two tiles of one sequence and key head, or one where two would
+// leave SMs idle, and (a slice of) their keys; the tensor core works on one tile while
+// the other's softmax runs.
 // Tiles lie in tensor memory: S 2 x 128 columns, O 2 x 128; P overlays S as the A
 // operand of its product.  A CTA an SM takes units until none is left: the grid
 // has one CTA a unit, and a running one cancels the next that has not started and
@@ -24,18 +25,19 @@
 // of four warps have a tile's softmax, a thread a row: maximum and sum stay in
 // registers.  A tile's products have one issuing thread and complete in order, so a
 // full S says that the product before it, which read P and V, is done too.  Where
-// a sequence has rows for one tile only, the second tile is the same rows again with
+// a unit has rows for one tile only, the second tile is the same rows again with
 // every other tile of keys, joined in the CTA at the end.  Slices' partial outputs are
-// joined by their LSEs in a second kernel.
+// joined by their references and sums in a second kernel.
 //
 // What bounds it.  Over many keys power (1,380 of 1,400 W) and the chain score,
 // softmax, product of each tile, which the other tile's hides in part: 16,384 tokens
-// x 16 heads x 192 / 128 causal 805 us, 1,710 TFLOP/s, of 128 / 128 693 us, 1,590;
-// 6,000 x 192 / 128 134 us, 1,370 (the tensor pipe active in 61 % of the cycles).
+// x 16 heads x 192 / 128 causal 805 to 860 us by the GPU, 1,600 to 1,710 TFLOP/s, of 128 /
+// 128 693 to 730 us, 1,510 to 1,590; 6,000 x 192 / 128 133 us, 1,380 (the tensor pipe
+// active in 61 % of the cycles).
 // The same with one CTA a unit 163, units taken in turn 156, a product warp a tile
 // and maxima from the loads 144, exponentials in turn 134.  Short prompts (16 packed
 // ones of up to 1,500 tokens, 160 us) pay each unit's last softmax and output, 3 to 4
-// us; single tokens walk memory: 32 over up to 8,192 keys x 64 / 8 heads 115 us, 5,450
+// us; single tokens walk memory: 32 over up to 8,192 keys x 64 / 8 heads 115 us, 5,430
 // GB/s (124 with their tiles of keys one after the other); one over 8,192 x 32 / 8 17.
 //
 // Values that a row must not see.  A weight of 0 does not keep an infinity or
@@ -88,8 +90,8 @@ constexpr int kMaskedTiles = 3;
 constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
 static_assert(128 * kFewRegs + 256 * kManyRegs == kThreads * kLaunchRegs, "registers");
 
-// Two tiles of a sequence's query tokens, one key head, tiles of keys [begin, begin +
-// count[s]) for tile s.
+// One or two tiles of a sequence's query tokens, one key head, tiles of keys [begin, begin
+// + count[s]) for tile s.
 struct Unit {
   int q0, nq;  // the sequence's first query token and their number
   int k0, nk;
@@ -1042,7 +1044,8 @@ PromptPlan plan_prompt_attention(int64_t q_tokens, int64_t kv_tokens, int batch,
     }
   }
   // A tile without rows waits for as long as the other's whole slice: no slice may last as
-  // long as a bounded wait (a tile of keys takes about 2 us, the wait a second at most).
+  // long as a bounded wait (a tile of keys takes about 2 us, the longest slice so 0.15 s; the
+  // wait gave up after 1.1 s where nothing ever came).
   const int64_t least = ((kv_tokens + kTile - 1) / kTile + kMaxSlice - 1) / kMaxSlice;
   if (p.splits < least) p.splits = static_cast<int>(least);
   // turns: both tiles filled, and 40 tiles of keys a slice or more, on average (without and with:
